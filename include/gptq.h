@@ -89,7 +89,7 @@ typedef struct gptq_config {
 const char *gptq_status_string(int32_t status);
 
 /* Library ABI version (major * 10000 + minor * 100 + patch); 200 added
- * gptq_config.pure_minmax. */
+ * gptq_config.pure_minmax, 300 the products with an epilogue. */
 int32_t gptq_version(void);
 
 /* Number of CUDA kernels this library has launched in this process since it
@@ -360,6 +360,76 @@ gptq_status gptq_dequant_gemm(const uint16_t *X, int64_t n_tok, int64_t d_col, i
 /* Workspace bytes gptq_dequant_gemm needs (n_tok x d_col bf16); 0 for invalid
  * sizes. */
 size_t gptq_dequant_gemm_workspace_size(int64_t n_tok, int64_t d_col);
+
+/* Activations of the products with an epilogue (erf and tanh forms of GELU). */
+typedef enum gptq_activation {
+    GPTQ_ACT_NONE = 0,
+    GPTQ_ACT_RELU = 1,
+    GPTQ_ACT_GELU = 2,       /* x Phi(x)                                              */
+    GPTQ_ACT_GELU_TANH = 3,  /* x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) / 2       */
+    GPTQ_ACT_SILU = 4        /* x / (1 + exp(-x))                                     */
+} gptq_activation;
+
+/*
+ * Products with packed layers that carry their epilogue.  The GPTQ pages stop
+ * at the product ("Limitations", items 1-2); these entry points do the work a
+ * transformer block has around it in the product's own kernel:
+ *
+ *   linear  Y[t][n] = act( sum_k X[t][perm[k]] W[n][k] + bias[n] ) + residual[t][n]
+ *   gated   Y[t][n] = act( sum_k X[t][perm[k]] Wg[n][k] ) * sum_k X[t][perm[k]] Wu[n][k]
+ *
+ * Common to all of them:
+ *   X, packed, scales, zeros, perm, ldx  as gptq_dequant_matmul; packed
+ *           16-byte aligned.  The gated form's two layers share X, and with it
+ *           perm, d_row, bits and group_size (layers that share their input
+ *           share its Hessian and so their act-order).
+ *   Y       n_tok x d_row bf16 (raw bit patterns), leading dimension
+ *           ldy >= d_row, overwritten: sums, bias, activation, gate product and
+ *           residual in fp32, rounded to bf16 once.
+ *   bias    fp32[d_row], or NULL.
+ *   residual  n_tok x d_row bf16, leading dimension ldr >= d_row, or NULL; may
+ *           be Y itself with ldr == ldy (the residual stream updated in
+ *           place).  No other output may overlap an input.
+ *   activation  a gptq_activation.
+ *   Supported: bits 2, 3, 4 or 8; d_col a multiple of 64 (128 at 3 bits) and at
+ *   most 2^24; d_row at most 2^24; the quantizer's group sizes (-1, >= d_col, 8,
+ *   16, 32, 64 or a multiple of 128); otherwise GPTQ_ERR_UNSUPPORTED.  X, Y and
+ *   residual rows of any alignment and stride.  n_tok == 0 is a no-op, and
+ *   nothing outside the n_tok x d_row entries of an output is written.
+ *   An infinite or NaN activation makes its token's outputs NaN (or infinite);
+ *   other tokens are unaffected.
+ *   Deterministic (no atomics); may be captured in a CUDA graph.  Calls that
+ *   overlap on the GPU (two streams, two captured graphs) need a workspace each.
+ *   Errors: GPTQ_ERR_INVALID_ARG for NULL pointers, bad sizes, strides or
+ *   alignment, an invalid bits, group size or activation; GPTQ_ERR_WORKSPACE
+ *   for a missing, misaligned (256 bytes) or small workspace where one is needed.
+ */
+
+/*
+ * Decode form, for a few tokens: tokens are taken up to 32 per launch and each
+ * launch reads the packed layer once.  W[n][k] = scales[k/g][n] * (code[n][k] -
+ * zeros[k/g][n]) enters unrounded, as in gptq_dequant_matmul.
+ *   ws  gptq_dequant_matmul_linear_workspace_size(n_tok, d_col) bytes, used when
+ *       perm is given or X's rows are not 16-byte aligned; may be NULL otherwise.
+ */
+gptq_status gptq_dequant_matmul_linear(const uint16_t *X, int64_t n_tok, int64_t d_col,
+                                       int64_t ldx, const uint32_t *packed, const float *scales,
+                                       const int32_t *zeros, const int32_t *perm, int64_t d_row,
+                                       int32_t bits, int32_t group_size, const float *bias,
+                                       int32_t activation, const uint16_t *residual, int64_t ldr,
+                                       uint16_t *Y, int64_t ldy, void *ws, size_t ws_bytes,
+                                       cudaStream_t stream);
+gptq_status gptq_dequant_matmul_gated(const uint16_t *X, int64_t n_tok, int64_t d_col, int64_t ldx,
+                                      const uint32_t *packed_gate, const float *scales_gate,
+                                      const int32_t *zeros_gate, const uint32_t *packed_up,
+                                      const float *scales_up, const int32_t *zeros_up,
+                                      const int32_t *perm, int64_t d_row, int32_t bits,
+                                      int32_t group_size, int32_t activation, uint16_t *Y,
+                                      int64_t ldy, void *ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Workspace bytes of the two (up to 32 tokens x d_col bf16); 0 for invalid sizes. */
+size_t gptq_dequant_matmul_linear_workspace_size(int64_t n_tok, int64_t d_col);
+size_t gptq_dequant_matmul_gated_workspace_size(int64_t n_tok, int64_t d_col);
 
 /*
  * Waits for `stream`, then copies the device status word to *out.

@@ -17,6 +17,8 @@ Stages (see the header for the exact contracts):
 * ``gptq_pack``                codes -> uint32 bit stream (8 codes per word at 4 bits)
 * ``gptq_dequant_matmul``      Y = X W_hat^T from the packed layer (decode form)
 * ``gptq_dequant_gemm``        the same for many tokens on the tensor cores (bf16 W_hat)
+* ``gptq_dequant_matmul_linear`` / ``_gated``  the decode form with its epilogue, bf16 Y:
+  act(X W^T + bias) + residual, and act(X Wg^T) * (X Wu^T) for a gated feed-forward block
 """
 from __future__ import annotations
 
@@ -29,6 +31,8 @@ __all__ = [
     "GPTQConfig", "GPTQError", "gptq_hessian_accumulate", "gptq_hessian_accumulate_host",
     "gptq_hessian_staging_size", "gptq_prepare_hinv", "gptq_dequant_matmul", "gptq_dequant_matmul_workspace_size",
     "gptq_dequant_gemm", "gptq_dequant_gemm_workspace_size",
+    "gptq_dequant_matmul_linear", "gptq_dequant_matmul_linear_workspace_size",
+    "gptq_dequant_matmul_gated", "gptq_dequant_matmul_gated_workspace_size", "ACTIVATIONS",
     "gptq_quantize_layer", "gptq_quantize_layer_noalloc", "gptq_noalloc_scratch_bytes", "gptq_pack", "gptq_workspace_size", "gptq_sync_status",
     "gptq_status_string", "gptq_version", "gptq_launch_counter", "gptq_debug_arm_wait_probe",
     "library_path", "n_groups", "packed_words",
@@ -41,6 +45,9 @@ _LIB_PATH = os.path.join(_HERE, "libgptq_b200.so")
 STATUS = {0: "GPTQ_OK", 1: "GPTQ_ERR_INVALID_ARG", 2: "GPTQ_ERR_UNSUPPORTED",
           3: "GPTQ_ERR_NOT_PD", 4: "GPTQ_ERR_TIMEOUT", 5: "GPTQ_ERR_CUDA",
           6: "GPTQ_ERR_WORKSPACE"}
+
+# gptq_activation, by name
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
 
 class GPTQConfig(ctypes.Structure):
@@ -94,6 +101,12 @@ def _load():
         "gptq_dequant_gemm": ([P, i64, i64, i64, P, P, P, P, i64, i32, i32, P, i64, P, P,
                                ctypes.c_size_t, P], ctypes.c_int),
         "gptq_dequant_gemm_workspace_size": ([i64, i64], ctypes.c_size_t),
+        "gptq_dequant_matmul_linear": ([P, i64, i64, i64, P, P, P, P, i64, i32, i32, P, i32, P, i64,
+                                        P, i64, P, ctypes.c_size_t, P], ctypes.c_int),
+        "gptq_dequant_matmul_linear_workspace_size": ([i64, i64], ctypes.c_size_t),
+        "gptq_dequant_matmul_gated": ([P, i64, i64, i64, P, P, P, P, P, P, P, i64, i32, i32, i32,
+                                       P, i64, P, ctypes.c_size_t, P], ctypes.c_int),
+        "gptq_dequant_matmul_gated_workspace_size": ([i64, i64], ctypes.c_size_t),
         "gptq_quantize_layer_noalloc": ([P, i64, i64, i64, P, P, P, cfgp, P, P, P, P, P],
                                         ctypes.c_int),
         "gptq_noalloc_scratch_bytes": ([], ctypes.c_size_t),
@@ -396,6 +409,142 @@ def gptq_dequant_gemm(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tenso
 
 def gptq_dequant_gemm_workspace_size(n_tok: int, d_col: int) -> int:
     return int(_lib.gptq_dequant_gemm_workspace_size(int(n_tok), int(d_col)))
+
+
+def _activation(name) -> int:
+    if name not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {name!r}")
+    return ACTIVATIONS[name]
+
+
+def _bytes(ws: torch.Tensor | None) -> int:
+    return 0 if ws is None else ws.numel() * ws.element_size()
+
+
+def _packed_layer(X: torch.Tensor, x_name: str, packed, scales, zeros, bits: int, group_size: int,
+                  d_col: int, suffix: str = "") -> int:
+    """Checks the shapes of one packed layer whose input width is d_col, and
+    returns its d_row."""
+    _cuda(packed, "packed" + suffix, torch.int32)
+    _cuda(scales, "scales" + suffix, torch.float32)
+    _cuda(zeros, "zeros" + suffix, torch.int32)
+    _same_device(X, x_name, (packed, "packed" + suffix, None), (scales, "scales" + suffix, None),
+                 (zeros, "zeros" + suffix, None))
+    for t, name in ((packed, "packed"), (scales, "scales"), (zeros, "zeros")):
+        if not t.is_contiguous():
+            raise ValueError(f"{name}{suffix} must be contiguous")
+    if int(group_size) < 1 and int(group_size) != -1:
+        return packed.shape[0]   # the library's own refusal follows
+    d_row = packed.shape[0]
+    ng = n_groups(d_col, int(group_size))
+    if tuple(packed.shape) != (d_row, packed_words(d_col, int(bits))):
+        raise ValueError(f"packed{suffix} must be d_row x {packed_words(d_col, int(bits))} words, "
+                         f"got {tuple(packed.shape)}")
+    for t, name in ((scales, "scales"), (zeros, "zeros")):
+        if tuple(t.shape) != (ng, d_row):
+            raise ValueError(f"{name}{suffix} must be {ng} x {d_row}, got {tuple(t.shape)}")
+    return d_row
+
+
+def _rows(ref: torch.Tensor, ref_name: str, t: torch.Tensor | None, name: str, n: int,
+          cols: int) -> int:
+    """An n x cols bf16 matrix with contiguous rows on ref's device (None
+    passes); returns its leading dimension."""
+    if t is None:
+        return 0
+    _cuda(t, name, torch.bfloat16)
+    _same_device(ref, ref_name, (t, name, None))
+    if tuple(t.shape) != (n, cols):
+        raise ValueError(f"{name} must be {n} x {cols}, got {tuple(t.shape)}")
+    return _leading(t, name)
+
+
+def _leading(t: torch.Tensor, name: str) -> int:
+    """_row_major for an operand that may be written or be one row of a wider
+    buffer: a stride below the row length (an expanded tensor) is refused."""
+    ld = _row_major(t, name)
+    if t.shape[0] > 1 and ld < t.shape[1]:
+        raise ValueError(f"the rows of {name} overlap (strides {t.stride()})")
+    return ld if t.shape[0] > 1 else t.shape[1]
+
+
+def _vector(ref: torch.Tensor, ref_name: str, t: torch.Tensor | None, name: str, n: int) -> None:
+    if t is None:
+        return
+    _cuda(t, name, torch.float32)
+    _same_device(ref, ref_name, (t, name, None))
+    if tuple(t.shape) != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous vector of {n}")
+
+
+def _order(ref: torch.Tensor, ref_name: str, perm: torch.Tensor | None, d_col: int) -> None:
+    if perm is None:
+        return
+    _cuda(perm, "perm", torch.int32)
+    _same_device(ref, ref_name, (perm, "perm", None))
+    if tuple(perm.shape) != (d_col,) or not perm.is_contiguous():
+        raise ValueError(f"perm must be a contiguous vector of {d_col}")
+
+
+def gptq_dequant_matmul_linear(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor,
+                               zeros: torch.Tensor, perm: torch.Tensor | None, bits: int,
+                               group_size: int, Y: torch.Tensor, ws: torch.Tensor | None = None,
+                               bias: torch.Tensor | None = None, activation: str = "none",
+                               residual: torch.Tensor | None = None, stream=None) -> None:
+    """Y = act(X W_hat^T + bias) + residual for a few tokens (decode form): X
+    (tokens x d_col bf16, original column order), packed / scales / zeros /
+    perm as the quantizer wrote them, bias fp32, residual and Y tokens x d_row
+    bf16 (residual may be Y itself); ws (bytes of
+    gptq_dequant_matmul_linear_workspace_size) is needed with a permutation
+    or when X's rows are not 16-byte aligned."""
+    _cuda(X, "X", torch.bfloat16)
+    ldx = _leading(X, "X")
+    n_tok, d_col = X.shape
+    d_row = _packed_layer(X, "X", packed, scales, zeros, bits, group_size, d_col)
+    _order(X, "X", perm, d_col)
+    _vector(X, "X", bias, "bias", d_row)
+    ldr = _rows(X, "X", residual, "residual", n_tok, d_row)
+    ldy = _rows(X, "X", Y, "Y", n_tok, d_row)
+    _same_device(X, "X", (ws, "ws", None))
+    _check(_lib.gptq_dequant_matmul_linear(_ptr(X), n_tok, d_col, ldx, _ptr(packed), _ptr(scales),
+                                           _ptr(zeros), _ptr(perm), d_row, int(bits),
+                                           int(group_size), _ptr(bias), _activation(activation),
+                                           _ptr(residual), ldr, _ptr(Y), ldy, _ptr(ws), _bytes(ws),
+                                           _stream(stream)), "gptq_dequant_matmul_linear")
+
+
+def gptq_dequant_matmul_linear_workspace_size(n_tok: int, d_col: int) -> int:
+    return int(_lib.gptq_dequant_matmul_linear_workspace_size(int(n_tok), int(d_col)))
+
+
+def gptq_dequant_matmul_gated(X: torch.Tensor, packed_gate: torch.Tensor, scales_gate: torch.Tensor,
+                              zeros_gate: torch.Tensor, packed_up: torch.Tensor,
+                              scales_up: torch.Tensor, zeros_up: torch.Tensor,
+                              perm: torch.Tensor | None, bits: int, group_size: int,
+                              activation: str, Y: torch.Tensor, ws: torch.Tensor | None = None,
+                              stream=None) -> None:
+    """Y = act(X Wg_hat^T) * (X Wu_hat^T) for a few tokens (decode form): two
+    packed layers that share X, perm, bits and group_size; Y tokens x d_row
+    bf16; ws as gptq_dequant_matmul_linear."""
+    _cuda(X, "X", torch.bfloat16)
+    ldx = _leading(X, "X")
+    n_tok, d_col = X.shape
+    d_row = _packed_layer(X, "X", packed_gate, scales_gate, zeros_gate, bits, group_size, d_col, "_gate")
+    if _packed_layer(X, "X", packed_up, scales_up, zeros_up, bits, group_size, d_col, "_up") != d_row:
+        raise ValueError("packed_gate and packed_up must have the same number of rows")
+    _order(X, "X", perm, d_col)
+    ldy = _rows(X, "X", Y, "Y", n_tok, d_row)
+    _same_device(X, "X", (ws, "ws", None))
+    _check(_lib.gptq_dequant_matmul_gated(_ptr(X), n_tok, d_col, ldx, _ptr(packed_gate),
+                                          _ptr(scales_gate), _ptr(zeros_gate), _ptr(packed_up),
+                                          _ptr(scales_up), _ptr(zeros_up), _ptr(perm), d_row,
+                                          int(bits), int(group_size), _activation(activation),
+                                          _ptr(Y), ldy, _ptr(ws), _bytes(ws), _stream(stream)),
+           "gptq_dequant_matmul_gated")
+
+
+def gptq_dequant_matmul_gated_workspace_size(n_tok: int, d_col: int) -> int:
+    return int(_lib.gptq_dequant_matmul_gated_workspace_size(int(n_tok), int(d_col)))
 
 
 def gptq_debug_arm_wait_probe(kernel: int, limit_ns: int) -> None:

@@ -1,0 +1,59 @@
+// Activations of the products with a packed layer, and their slopes, in fp32
+// (gptq_activation in the header).  Each is written so that no intermediate
+// value overflows into a NaN for a finite x, and so that the small values left
+// of zero keep their relative accuracy (erfc and 1 / (1 + exp) instead of
+// 1 + erf and 1 + tanh).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "../../include/gptq.h"
+
+namespace gptq {
+
+constexpr float kSqrt2OverPi = 0.79788456080286535588f;
+constexpr float kInvSqrt2 = 0.70710678118654752440f;
+constexpr float kInvSqrt2Pi = 0.39894228040143267794f;
+constexpr float kGeluCubic = 0.044715f;
+
+// exp(-x) overflows to +inf for x < -88: the quotient is then -0
+__device__ __forceinline__ float sigmoid_f(float x) { return 1.f / (1.f + expf(-x)); }
+
+// (1 + tanh(u)) / 2 = 1 / (1 + exp(-2u)), u = sqrt(2/pi) (x + 0.044715 x^3)
+__device__ __forceinline__ float gelu_tanh_half(float x) {
+    const float u = kSqrt2OverPi * (x + kGeluCubic * x * x * x);
+    return 1.f / (1.f + expf(-2.f * u));
+}
+
+__device__ __forceinline__ float activate(float x, int act) {
+    switch (act) {
+        case GPTQ_ACT_RELU: return x < 0.f ? 0.f : x;  // a NaN stays one
+        case GPTQ_ACT_GELU: return 0.5f * x * erfcf(-x * kInvSqrt2);
+        case GPTQ_ACT_GELU_TANH: return x * gelu_tanh_half(x);
+        case GPTQ_ACT_SILU: return x * sigmoid_f(x);
+        default: return x;
+    }
+}
+
+__device__ __forceinline__ float activate_slope(float x, int act) {
+    switch (act) {
+        case GPTQ_ACT_RELU: return x > 0.f ? 1.f : 0.f;
+        case GPTQ_ACT_GELU:
+            return 0.5f * erfcf(-x * kInvSqrt2) + x * kInvSqrt2Pi * expf(-0.5f * x * x);
+        case GPTQ_ACT_GELU_TANH: {
+            const float h = gelu_tanh_half(x), p = h * (1.f - h);
+            // p is 0 where x^2 may overflow
+            return p == 0.f ? h
+                            : h + 2.f * x * p * kSqrt2OverPi * (1.f + 3.f * kGeluCubic * x * x);
+        }
+        case GPTQ_ACT_SILU: {
+            const float s = sigmoid_f(x);
+            // x s (1 - s) with s = 0 or 1 beyond |x| = 88 / 17 (x may be infinite there)
+            const float p = s * (1.f - s);
+            return p == 0.f ? s : s + x * p;
+        }
+        default: return 1.f;
+    }
+}
+
+}  // namespace gptq

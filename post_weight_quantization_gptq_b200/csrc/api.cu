@@ -72,6 +72,39 @@ gptq_status check_config(const gptq_config* cfg, int64_t d_col) {
     return (g % cfg->block_size == 0) ? GPTQ_OK : GPTQ_ERR_UNSUPPORTED;
 }
 
+// A packed layer of the products with an epilogue: what gptq_pack and
+// gptq_quantize_layer write for a quantizer's group sizes.
+gptq_status check_packed(const uint32_t* packed, const float* scales, const int32_t* zeros) {
+    if (packed == nullptr || scales == nullptr || zeros == nullptr) return GPTQ_ERR_INVALID_ARG;
+    if (!aligned(packed, 16) || !aligned(scales, 4) || !aligned(zeros, 4)) return GPTQ_ERR_INVALID_ARG;
+    return GPTQ_OK;
+}
+
+gptq_status check_shape(int64_t n_tok, int64_t d_col, int64_t d_row, int32_t bits,
+                        int32_t group_size, int32_t activation, const int32_t* perm) {
+    if (n_tok < 0 || n_tok > (int64_t{1} << 24) || d_col <= 0 || d_row <= 0) return GPTQ_ERR_INVALID_ARG;
+    if (bits != 2 && bits != 3 && bits != 4 && bits != 8) return GPTQ_ERR_INVALID_ARG;
+    if (group_size == 0 || group_size < -1) return GPTQ_ERR_INVALID_ARG;
+    if (activation < GPTQ_ACT_NONE || activation > GPTQ_ACT_SILU) return GPTQ_ERR_INVALID_ARG;
+    if (!aligned(perm, 4)) return GPTQ_ERR_INVALID_ARG;
+    if (d_col > (int64_t{1} << 24) || d_row > (int64_t{1} << 24)) return GPTQ_ERR_UNSUPPORTED;
+    // packed rows of whole 16-byte units and whole steps of codes
+    if (d_col % (bits == 3 ? 128 : 64) != 0) return GPTQ_ERR_UNSUPPORTED;
+    const int32_t g = group_size;
+    if (g != -1 && g < d_col && g % 128 != 0 && g != 8 && g != 16 && g != 32 && g != 64)
+        return GPTQ_ERR_UNSUPPORTED;
+    return GPTQ_OK;
+}
+
+// A bf16 matrix of the caller: rows of `cols` elements, any alignment.
+bool bad_rows(const uint16_t* p, int64_t ld, int64_t cols) {
+    return p == nullptr || ld < cols || !aligned(p, 2);
+}
+
+bool small_ws(const void* ws, size_t have, size_t need) {
+    return need > 0 && (ws == nullptr || !aligned(ws, 256) || have < need);
+}
+
 gptq_status launch_status(gptq_status s) {
     if (s != GPTQ_OK) return s;
     return cudaGetLastError() == cudaSuccess ? GPTQ_OK : GPTQ_ERR_CUDA;
@@ -94,7 +127,7 @@ const char* gptq_status_string(int32_t status) {
     }
 }
 
-int32_t gptq_version(void) { return 200; }
+int32_t gptq_version(void) { return 300; }
 
 gptq_status gptq_debug_arm_wait_probe(int32_t kernel, int64_t limit_ns) {
     if ((kernel != 1 && kernel != 2) || limit_ns <= 0 || limit_ns > 1000000000) return GPTQ_ERR_INVALID_ARG;
@@ -267,6 +300,64 @@ gptq_status gptq_dequant_gemm(const uint16_t* X, int64_t n_tok, int64_t d_col, i
     return launch_status(gptq::launch_dequant_gemm(X, n_tok, d_col, ldx, packed, scales, zeros, perm,
                                                    d_row, bits, group_size, Y, ldy, dev_status, ws,
                                                    stream));
+}
+
+size_t gptq_dequant_matmul_linear_workspace_size(int64_t n_tok, int64_t d_col) {
+    if (n_tok <= 0 || d_col <= 0 || d_col > kMaxDim) return 0;
+    return gptq::linear_decode_workspace_bytes(n_tok, d_col);
+}
+
+size_t gptq_dequant_matmul_gated_workspace_size(int64_t n_tok, int64_t d_col) {
+    return gptq_dequant_matmul_linear_workspace_size(n_tok, d_col);
+}
+
+gptq_status gptq_dequant_matmul_linear(const uint16_t* X, int64_t n_tok, int64_t d_col, int64_t ldx,
+                                       const uint32_t* packed, const float* scales,
+                                       const int32_t* zeros, const int32_t* perm, int64_t d_row,
+                                       int32_t bits, int32_t group_size, const float* bias,
+                                       int32_t activation, const uint16_t* residual, int64_t ldr,
+                                       uint16_t* Y, int64_t ldy, void* ws, size_t ws_bytes,
+                                       cudaStream_t stream) {
+    gptq_status c = check_packed(packed, scales, zeros);
+    if (c == GPTQ_OK) c = check_shape(n_tok, d_col, d_row, bits, group_size, activation, perm);
+    if (c != GPTQ_OK || n_tok == 0) return c;
+    if (bad_rows(X, ldx, d_col) || bad_rows(Y, ldy, d_row)) return GPTQ_ERR_INVALID_ARG;
+    if (residual != nullptr && bad_rows(residual, ldr, d_row)) return GPTQ_ERR_INVALID_ARG;
+    if (!aligned(bias, 4)) return GPTQ_ERR_INVALID_ARG;
+    if (gptq::needs_gather(X, ldx, perm) &&
+        small_ws(ws, ws_bytes, gptq::linear_decode_workspace_bytes(n_tok, d_col)))
+        return GPTQ_ERR_WORKSPACE;
+    gptq::LinearCall a = {};
+    a.X = X; a.n_tok = n_tok; a.d_col = d_col; a.ldx = ldx;
+    a.mat[0] = {packed, scales, zeros};
+    a.perm = perm; a.d_row = d_row; a.bits = bits; a.group = group_size;
+    a.bias = bias; a.act = activation; a.residual = residual; a.ldr = ldr;
+    a.Y = Y; a.ldy = ldy; a.ws = ws;
+    return launch_status(gptq::launch_linear_decode(a, stream));
+}
+
+gptq_status gptq_dequant_matmul_gated(const uint16_t* X, int64_t n_tok, int64_t d_col, int64_t ldx,
+                                      const uint32_t* packed_gate, const float* scales_gate,
+                                      const int32_t* zeros_gate, const uint32_t* packed_up,
+                                      const float* scales_up, const int32_t* zeros_up,
+                                      const int32_t* perm, int64_t d_row, int32_t bits,
+                                      int32_t group_size, int32_t activation, uint16_t* Y,
+                                      int64_t ldy, void* ws, size_t ws_bytes, cudaStream_t stream) {
+    gptq_status c = check_packed(packed_gate, scales_gate, zeros_gate);
+    if (c == GPTQ_OK) c = check_packed(packed_up, scales_up, zeros_up);
+    if (c == GPTQ_OK) c = check_shape(n_tok, d_col, d_row, bits, group_size, activation, perm);
+    if (c != GPTQ_OK || n_tok == 0) return c;
+    if (bad_rows(X, ldx, d_col) || bad_rows(Y, ldy, d_row)) return GPTQ_ERR_INVALID_ARG;
+    if (gptq::needs_gather(X, ldx, perm) &&
+        small_ws(ws, ws_bytes, gptq::linear_decode_workspace_bytes(n_tok, d_col)))
+        return GPTQ_ERR_WORKSPACE;
+    gptq::LinearCall a = {};
+    a.X = X; a.n_tok = n_tok; a.d_col = d_col; a.ldx = ldx;
+    a.mat[0] = {packed_gate, scales_gate, zeros_gate};
+    a.mat[1] = {packed_up, scales_up, zeros_up};
+    a.perm = perm; a.d_row = d_row; a.bits = bits; a.group = group_size;
+    a.act = activation; a.Y = Y; a.ldy = ldy; a.ws = ws;
+    return launch_status(gptq::launch_linear_decode(a, stream));
 }
 
 gptq_status gptq_sync_status(cudaStream_t stream, const int32_t* dev_status, int32_t* out) {

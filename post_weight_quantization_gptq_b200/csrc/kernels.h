@@ -108,6 +108,41 @@ gptq_status launch_dequant_gemm(const uint16_t* X, int64_t n_tok, int64_t d_col,
                                 const int32_t* perm, int64_t d_row, int bits, int group, float* Y,
                                 int64_t ldy, int32_t* status, void* ws, cudaStream_t stream);
 
+// ---- products with packed layers that carry their epilogue.  mat[1] is given
+// by the gated form only (gate, up), pre by the callers that keep the
+// products' own outputs.
+struct PackedMatrix {
+    const uint32_t* packed;
+    const float* scales;
+    const int32_t* zeros;
+};
+struct LinearCall {
+    const uint16_t* X;
+    int64_t n_tok, d_col, ldx;
+    PackedMatrix mat[2];
+    const int32_t* perm;
+    int64_t d_row;
+    int bits, group;
+    const float* bias;
+    int act;
+    const uint16_t* residual;
+    int64_t ldr;
+    uint16_t* pre[2];
+    int64_t ldpre[2];
+    uint16_t* Y;
+    int64_t ldy;
+    int32_t* status;
+    void* ws;
+};
+// X's rows reach the kernels by 16-byte loads in quantization order
+inline bool needs_gather(const uint16_t* X, int64_t ldx, const int32_t* perm) {
+    return perm != nullptr || (ldx % 8) != 0 || (reinterpret_cast<uintptr_t>(X) & 15) != 0;
+}
+
+// ---- decode form (linear_decode.cu)
+size_t linear_decode_workspace_bytes(int64_t n_tok, int64_t d_col);
+gptq_status launch_linear_decode(const LinearCall& c, cudaStream_t stream);
+
 // ---- stage 5 (pack.cu)
 gptq_status launch_pack(const uint8_t* codes, int64_t d_row, int64_t d_col, int bits,
                         uint32_t* packed, cudaStream_t stream);
