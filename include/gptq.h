@@ -432,6 +432,90 @@ size_t gptq_dequant_matmul_linear_workspace_size(int64_t n_tok, int64_t d_col);
 size_t gptq_dequant_matmul_gated_workspace_size(int64_t n_tok, int64_t d_col);
 
 /*
+ * Many-token form on the tensor cores.  The weights enter as the 16-bit numbers
+ * W[n][k] = bf16_rne( fp32 scales[k/g][n] * (code[n][k] - zeros[k/g][n]) ), as in
+ * gptq_dequant_gemm; sums are fp32.
+ *   pre     linear, or NULL: n_tok x d_row bf16 output (leading dimension ldpre),
+ *           the sums with the bias, before the activation, rounded to bf16:
+ *           what the backward pass needs.
+ *   gate, up  gated, each or NULL: the two products, the same way.
+ *   dev_status  device int32 (may be NULL) receiving GPTQ_ERR_TIMEOUT if a
+ *           bounded wait runs out.
+ *   ws      *_workspace_size(n_tok, d_col, d_row) bytes: the tokens in
+ *           quantization order (perm given, or X's rows not 16-byte aligned) and
+ *           the parts of output tiles whose contraction is split over several
+ *           SMs.  May be NULL where neither happens.
+ */
+gptq_status gptq_dequant_gemm_linear(const uint16_t *X, int64_t n_tok, int64_t d_col, int64_t ldx,
+                                     const uint32_t *packed, const float *scales,
+                                     const int32_t *zeros, const int32_t *perm, int64_t d_row,
+                                     int32_t bits, int32_t group_size, const float *bias,
+                                     int32_t activation, const uint16_t *residual, int64_t ldr,
+                                     uint16_t *pre, int64_t ldpre, uint16_t *Y, int64_t ldy,
+                                     int32_t *dev_status, void *ws, size_t ws_bytes,
+                                     cudaStream_t stream);
+gptq_status gptq_dequant_gemm_gated(const uint16_t *X, int64_t n_tok, int64_t d_col, int64_t ldx,
+                                    const uint32_t *packed_gate, const float *scales_gate,
+                                    const int32_t *zeros_gate, const uint32_t *packed_up,
+                                    const float *scales_up, const int32_t *zeros_up,
+                                    const int32_t *perm, int64_t d_row, int32_t bits,
+                                    int32_t group_size, int32_t activation, uint16_t *gate,
+                                    int64_t ldgate, uint16_t *up, int64_t ldup, uint16_t *Y,
+                                    int64_t ldy, int32_t *dev_status, void *ws, size_t ws_bytes,
+                                    cudaStream_t stream);
+
+/* Workspace bytes of the two; 0 for invalid sizes. */
+size_t gptq_dequant_gemm_linear_workspace_size(int64_t n_tok, int64_t d_col, int64_t d_row);
+size_t gptq_dequant_gemm_gated_workspace_size(int64_t n_tok, int64_t d_col, int64_t d_row);
+
+/*
+ * Gradients of the many-token forms with respect to their inputs, for training
+ * what surrounds frozen packed layers (the packed weights have none):
+ *   linear  dP = dY * act'(pre);  dbias[n] = sum_t dP[t][n];
+ *           dX[t][perm[k]] = sum_n bf16(dP[t][n]) W[n][k]
+ *           (the residual's gradient is dY)
+ *   gated   dG = dY * up * act'(gate);  dU = dY * act(gate);
+ *           dX[t][perm[k]] = sum_n bf16(dG[t][n]) Wg[n][k] + bf16(dU[t][n]) Wu[n][k]
+ * W as in the many-token form, sums fp32, the slope of RELU at 0 is 0.
+ *   dY      n_tok x d_row bf16 (leading dimension lddy).
+ *   pre; gate, up  what the forward call saved, any alignment.
+ *   dPre; dGate, dUp  n_tok x d_row bf16 outputs with 16-byte aligned rows (the
+ *           tensor memory accelerator reads them): dP; dG, dU rounded to bf16 --
+ *           also the gradient that an adapter beside the layer needs.  dPre may
+ *           be NULL without an activation when dY's own rows are 16-byte
+ *           aligned.  Each may be one of dY, pre, gate, up itself (the same
+ *           pointer and leading dimension); dGate and dUp are apart.
+ *   dbias   fp32[d_row] output, or NULL (sums of the unrounded dP).
+ *   dX      n_tok x d_col bf16 output (leading dimension lddx), original column
+ *           order; perm has to be a permutation (entries outside [0, d_col) are
+ *           read as k and the values are then unspecified; no access leaves the
+ *           buffers).
+ *   dev_status  as above.
+ *   ws      *_workspace_size(n_tok, d_col, d_row) bytes, used with a
+ *           permutation, with dbias and for split tiles.
+ *   n_tok == 0 writes nothing but a zero dbias.
+ */
+gptq_status gptq_dequant_gemm_linear_backward(
+    const uint16_t *dY, int64_t n_tok, int64_t d_row, int64_t lddy, const uint32_t *packed,
+    const float *scales, const int32_t *zeros, const int32_t *perm, int64_t d_col, int32_t bits,
+    int32_t group_size, int32_t activation, const uint16_t *pre, int64_t ldpre, uint16_t *dPre,
+    int64_t lddpre, float *dbias, uint16_t *dX, int64_t lddx, int32_t *dev_status, void *ws,
+    size_t ws_bytes, cudaStream_t stream);
+gptq_status gptq_dequant_gemm_gated_backward(
+    const uint16_t *dY, int64_t n_tok, int64_t d_row, int64_t lddy, const uint16_t *gate,
+    int64_t ldgate, const uint16_t *up, int64_t ldup, const uint32_t *packed_gate,
+    const float *scales_gate, const int32_t *zeros_gate, const uint32_t *packed_up,
+    const float *scales_up, const int32_t *zeros_up, const int32_t *perm, int64_t d_col,
+    int32_t bits, int32_t group_size, int32_t activation, uint16_t *dGate, int64_t lddgate,
+    uint16_t *dUp, int64_t lddup, uint16_t *dX, int64_t lddx, int32_t *dev_status, void *ws,
+    size_t ws_bytes, cudaStream_t stream);
+
+/* Workspace bytes of the two; 0 for invalid sizes. */
+size_t gptq_dequant_gemm_linear_backward_workspace_size(int64_t n_tok, int64_t d_col,
+                                                        int64_t d_row);
+size_t gptq_dequant_gemm_gated_backward_workspace_size(int64_t n_tok, int64_t d_col, int64_t d_row);
+
+/*
  * Waits for `stream`, then copies the device status word to *out.
  * Returns GPTQ_ERR_CUDA if the wait or the copy fails, else GPTQ_OK (the
  * device-side status itself is in *out).

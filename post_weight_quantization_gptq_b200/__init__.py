@@ -19,6 +19,8 @@ Stages (see the header for the exact contracts):
 * ``gptq_dequant_gemm``        the same for many tokens on the tensor cores (bf16 W_hat)
 * ``gptq_dequant_matmul_linear`` / ``_gated``  the decode form with its epilogue, bf16 Y:
   act(X W^T + bias) + residual, and act(X Wg^T) * (X Wu^T) for a gated feed-forward block
+* ``gptq_dequant_gemm_linear`` / ``_gated``  the same for many tokens on the tensor cores
+* ``gptq_dequant_gemm_linear_backward`` / ``_gated_backward``  their gradients
 """
 from __future__ import annotations
 
@@ -33,6 +35,10 @@ __all__ = [
     "gptq_dequant_gemm", "gptq_dequant_gemm_workspace_size",
     "gptq_dequant_matmul_linear", "gptq_dequant_matmul_linear_workspace_size",
     "gptq_dequant_matmul_gated", "gptq_dequant_matmul_gated_workspace_size", "ACTIVATIONS",
+    "gptq_dequant_gemm_linear", "gptq_dequant_gemm_linear_workspace_size",
+    "gptq_dequant_gemm_gated", "gptq_dequant_gemm_gated_workspace_size",
+    "gptq_dequant_gemm_linear_backward", "gptq_dequant_gemm_linear_backward_workspace_size",
+    "gptq_dequant_gemm_gated_backward", "gptq_dequant_gemm_gated_backward_workspace_size",
     "gptq_quantize_layer", "gptq_quantize_layer_noalloc", "gptq_noalloc_scratch_bytes", "gptq_pack", "gptq_workspace_size", "gptq_sync_status",
     "gptq_status_string", "gptq_version", "gptq_launch_counter", "gptq_debug_arm_wait_probe",
     "library_path", "n_groups", "packed_words",
@@ -107,6 +113,21 @@ def _load():
         "gptq_dequant_matmul_gated": ([P, i64, i64, i64, P, P, P, P, P, P, P, i64, i32, i32, i32,
                                        P, i64, P, ctypes.c_size_t, P], ctypes.c_int),
         "gptq_dequant_matmul_gated_workspace_size": ([i64, i64], ctypes.c_size_t),
+        "gptq_dequant_gemm_linear": ([P, i64, i64, i64, P, P, P, P, i64, i32, i32, P, i32, P, i64,
+                                      P, i64, P, i64, P, P, ctypes.c_size_t, P], ctypes.c_int),
+        "gptq_dequant_gemm_gated": ([P, i64, i64, i64, P, P, P, P, P, P, P, i64, i32, i32, i32,
+                                     P, i64, P, i64, P, i64, P, P, ctypes.c_size_t, P],
+                                    ctypes.c_int),
+        "gptq_dequant_gemm_linear_backward": ([P, i64, i64, i64, P, P, P, P, i64, i32, i32, i32, P,
+                                               i64, P, i64, P, P, i64, P, P, ctypes.c_size_t, P],
+                                              ctypes.c_int),
+        "gptq_dequant_gemm_gated_backward": ([P, i64, i64, i64, P, i64, P, i64, P, P, P, P, P, P, P,
+                                              i64, i32, i32, i32, P, i64, P, i64, P, i64, P, P,
+                                              ctypes.c_size_t, P], ctypes.c_int),
+        "gptq_dequant_gemm_linear_workspace_size": ([i64, i64, i64], ctypes.c_size_t),
+        "gptq_dequant_gemm_gated_workspace_size": ([i64, i64, i64], ctypes.c_size_t),
+        "gptq_dequant_gemm_linear_backward_workspace_size": ([i64, i64, i64], ctypes.c_size_t),
+        "gptq_dequant_gemm_gated_backward_workspace_size": ([i64, i64, i64], ctypes.c_size_t),
         "gptq_quantize_layer_noalloc": ([P, i64, i64, i64, P, P, P, cfgp, P, P, P, P, P],
                                         ctypes.c_int),
         "gptq_noalloc_scratch_bytes": ([], ctypes.c_size_t),
@@ -465,7 +486,7 @@ def _leading(t: torch.Tensor, name: str) -> int:
     ld = _row_major(t, name)
     if t.shape[0] > 1 and ld < t.shape[1]:
         raise ValueError(f"the rows of {name} overlap (strides {t.stride()})")
-    return ld if t.shape[0] > 1 else t.shape[1]
+    return ld
 
 
 def _vector(ref: torch.Tensor, ref_name: str, t: torch.Tensor | None, name: str, n: int) -> None:
@@ -545,6 +566,153 @@ def gptq_dequant_matmul_gated(X: torch.Tensor, packed_gate: torch.Tensor, scales
 
 def gptq_dequant_matmul_gated_workspace_size(n_tok: int, d_col: int) -> int:
     return int(_lib.gptq_dequant_matmul_gated_workspace_size(int(n_tok), int(d_col)))
+
+
+def gptq_dequant_gemm_linear(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor,
+                             zeros: torch.Tensor, perm: torch.Tensor | None, bits: int,
+                             group_size: int, Y: torch.Tensor, ws: torch.Tensor | None = None,
+                             bias: torch.Tensor | None = None, activation: str = "none",
+                             residual: torch.Tensor | None = None, pre: torch.Tensor | None = None,
+                             dev_status: torch.Tensor | None = None, stream=None) -> None:
+    """Y = act(X W_hat^T + bias) + residual for many tokens on the tensor cores
+    (W_hat as 16-bit weights): operands as gptq_dequant_matmul_linear; pre
+    (tokens x d_row bf16), if given, receives the sums before the activation
+    for the backward pass; ws of gptq_dequant_gemm_linear_workspace_size bytes."""
+    _cuda(X, "X", torch.bfloat16)
+    ldx = _leading(X, "X")
+    n_tok, d_col = X.shape
+    d_row = _packed_layer(X, "X", packed, scales, zeros, bits, group_size, d_col)
+    _order(X, "X", perm, d_col)
+    _vector(X, "X", bias, "bias", d_row)
+    ldr = _rows(X, "X", residual, "residual", n_tok, d_row)
+    ldpre = _rows(X, "X", pre, "pre", n_tok, d_row)
+    ldy = _rows(X, "X", Y, "Y", n_tok, d_row)
+    _same_device(X, "X", (ws, "ws", None), (dev_status, "dev_status", torch.int32))
+    _check(_lib.gptq_dequant_gemm_linear(_ptr(X), n_tok, d_col, ldx, _ptr(packed), _ptr(scales),
+                                         _ptr(zeros), _ptr(perm), d_row, int(bits), int(group_size),
+                                         _ptr(bias), _activation(activation), _ptr(residual), ldr,
+                                         _ptr(pre), ldpre, _ptr(Y), ldy, _ptr(dev_status), _ptr(ws),
+                                         _bytes(ws), _stream(stream)), "gptq_dequant_gemm_linear")
+
+
+def gptq_dequant_gemm_linear_workspace_size(n_tok: int, d_col: int, d_row: int) -> int:
+    return int(_lib.gptq_dequant_gemm_linear_workspace_size(int(n_tok), int(d_col), int(d_row)))
+
+
+def gptq_dequant_gemm_gated(X: torch.Tensor, packed_gate: torch.Tensor, scales_gate: torch.Tensor,
+                            zeros_gate: torch.Tensor, packed_up: torch.Tensor,
+                            scales_up: torch.Tensor, zeros_up: torch.Tensor,
+                            perm: torch.Tensor | None, bits: int, group_size: int, activation: str,
+                            Y: torch.Tensor, ws: torch.Tensor | None = None,
+                            gate: torch.Tensor | None = None, up: torch.Tensor | None = None,
+                            dev_status: torch.Tensor | None = None, stream=None) -> None:
+    """Y = act(X Wg_hat^T) * (X Wu_hat^T) for many tokens on the tensor cores,
+    both products, the activation and their product in one kernel; gate and
+    up (tokens x d_row bf16), if given, receive the two products for the
+    backward pass; ws of gptq_dequant_gemm_gated_workspace_size bytes."""
+    _cuda(X, "X", torch.bfloat16)
+    ldx = _leading(X, "X")
+    n_tok, d_col = X.shape
+    d_row = _packed_layer(X, "X", packed_gate, scales_gate, zeros_gate, bits, group_size, d_col, "_gate")
+    if _packed_layer(X, "X", packed_up, scales_up, zeros_up, bits, group_size, d_col, "_up") != d_row:
+        raise ValueError("packed_gate and packed_up must have the same number of rows")
+    _order(X, "X", perm, d_col)
+    ldg = _rows(X, "X", gate, "gate", n_tok, d_row)
+    ldu = _rows(X, "X", up, "up", n_tok, d_row)
+    ldy = _rows(X, "X", Y, "Y", n_tok, d_row)
+    _same_device(X, "X", (ws, "ws", None), (dev_status, "dev_status", torch.int32))
+    _check(_lib.gptq_dequant_gemm_gated(_ptr(X), n_tok, d_col, ldx, _ptr(packed_gate),
+                                        _ptr(scales_gate), _ptr(zeros_gate), _ptr(packed_up),
+                                        _ptr(scales_up), _ptr(zeros_up), _ptr(perm), d_row,
+                                        int(bits), int(group_size), _activation(activation),
+                                        _ptr(gate), ldg, _ptr(up), ldu, _ptr(Y), ldy,
+                                        _ptr(dev_status), _ptr(ws), _bytes(ws), _stream(stream)),
+           "gptq_dequant_gemm_gated")
+
+
+def gptq_dequant_gemm_gated_workspace_size(n_tok: int, d_col: int, d_row: int) -> int:
+    return int(_lib.gptq_dequant_gemm_gated_workspace_size(int(n_tok), int(d_col), int(d_row)))
+
+
+def gptq_dequant_gemm_linear_backward(dY: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor,
+                                      zeros: torch.Tensor, perm: torch.Tensor | None, bits: int,
+                                      group_size: int, dX: torch.Tensor,
+                                      ws: torch.Tensor | None = None, activation: str = "none",
+                                      pre: torch.Tensor | None = None,
+                                      dPre: torch.Tensor | None = None,
+                                      dbias: torch.Tensor | None = None,
+                                      dev_status: torch.Tensor | None = None, stream=None) -> None:
+    """Gradients of gptq_dequant_gemm_linear for its output gradient dY (tokens
+    x d_row bf16) and the saved pre: dPre = dY act'(pre) (bf16, 16-byte aligned
+    rows; may be None without an activation), dbias = its column sums (fp32,
+    optional), dX = dPre W_hat (tokens x d_col bf16, original column order); ws
+    of gptq_dequant_gemm_linear_backward_workspace_size bytes."""
+    _cuda(dY, "dY", torch.bfloat16)
+    lddy = _leading(dY, "dY")
+    n_tok, d_row = dY.shape
+    _cuda(dX, "dX", torch.bfloat16)
+    d_col = dX.shape[-1]
+    if _packed_layer(dY, "dY", packed, scales, zeros, bits, group_size, d_col) != d_row:
+        raise ValueError(f"packed must have dY's {d_row} columns as rows, got {packed.shape[0]}")
+    _order(dY, "dY", perm, d_col)
+    ldpre = _rows(dY, "dY", pre, "pre", n_tok, d_row)
+    lddp = _rows(dY, "dY", dPre, "dPre", n_tok, d_row)
+    _vector(dY, "dY", dbias, "dbias", d_row)
+    lddx = _rows(dY, "dY", dX, "dX", n_tok, d_col)
+    _same_device(dY, "dY", (ws, "ws", None), (dev_status, "dev_status", torch.int32))
+    _check(_lib.gptq_dequant_gemm_linear_backward(
+        _ptr(dY), n_tok, d_row, lddy, _ptr(packed), _ptr(scales), _ptr(zeros), _ptr(perm), d_col,
+        int(bits), int(group_size), _activation(activation), _ptr(pre), ldpre, _ptr(dPre), lddp,
+        _ptr(dbias), _ptr(dX), lddx, _ptr(dev_status), _ptr(ws), _bytes(ws), _stream(stream)),
+        "gptq_dequant_gemm_linear_backward")
+
+
+def gptq_dequant_gemm_linear_backward_workspace_size(n_tok: int, d_col: int, d_row: int) -> int:
+    return int(_lib.gptq_dequant_gemm_linear_backward_workspace_size(int(n_tok), int(d_col),
+                                                                     int(d_row)))
+
+
+def gptq_dequant_gemm_gated_backward(dY: torch.Tensor, gate: torch.Tensor, up: torch.Tensor,
+                                     packed_gate: torch.Tensor, scales_gate: torch.Tensor,
+                                     zeros_gate: torch.Tensor, packed_up: torch.Tensor,
+                                     scales_up: torch.Tensor, zeros_up: torch.Tensor,
+                                     perm: torch.Tensor | None, bits: int, group_size: int,
+                                     activation: str, dGate: torch.Tensor, dUp: torch.Tensor,
+                                     dX: torch.Tensor, ws: torch.Tensor | None = None,
+                                     dev_status: torch.Tensor | None = None, stream=None) -> None:
+    """Gradients of gptq_dequant_gemm_gated for its output gradient dY and the
+    saved gate and up products: dGate = dY up act'(gate), dUp = dY act(gate)
+    (bf16, 16-byte aligned rows), dX = dGate Wg_hat + dUp Wu_hat (tokens x d_col
+    bf16, original column order); ws of
+    gptq_dequant_gemm_gated_backward_workspace_size bytes."""
+    _cuda(dY, "dY", torch.bfloat16)
+    lddy = _leading(dY, "dY")
+    n_tok, d_row = dY.shape
+    _cuda(dX, "dX", torch.bfloat16)
+    d_col = dX.shape[-1]
+    for packed, scales, zeros, suffix in ((packed_gate, scales_gate, zeros_gate, "_gate"),
+                                          (packed_up, scales_up, zeros_up, "_up")):
+        if _packed_layer(dY, "dY", packed, scales, zeros, bits, group_size, d_col, suffix) != d_row:
+            raise ValueError(f"packed{suffix} must have dY's {d_row} columns as rows, "
+                             f"got {packed.shape[0]}")
+    _order(dY, "dY", perm, d_col)
+    ldg = _rows(dY, "dY", gate, "gate", n_tok, d_row)
+    ldu = _rows(dY, "dY", up, "up", n_tok, d_row)
+    lddg = _rows(dY, "dY", dGate, "dGate", n_tok, d_row)
+    lddu = _rows(dY, "dY", dUp, "dUp", n_tok, d_row)
+    lddx = _rows(dY, "dY", dX, "dX", n_tok, d_col)
+    _same_device(dY, "dY", (ws, "ws", None), (dev_status, "dev_status", torch.int32))
+    _check(_lib.gptq_dequant_gemm_gated_backward(
+        _ptr(dY), n_tok, d_row, lddy, _ptr(gate), ldg, _ptr(up), ldu, _ptr(packed_gate),
+        _ptr(scales_gate), _ptr(zeros_gate), _ptr(packed_up), _ptr(scales_up), _ptr(zeros_up),
+        _ptr(perm), d_col, int(bits), int(group_size), _activation(activation), _ptr(dGate), lddg,
+        _ptr(dUp), lddu, _ptr(dX), lddx, _ptr(dev_status), _ptr(ws), _bytes(ws), _stream(stream)),
+        "gptq_dequant_gemm_gated_backward")
+
+
+def gptq_dequant_gemm_gated_backward_workspace_size(n_tok: int, d_col: int, d_row: int) -> int:
+    return int(_lib.gptq_dequant_gemm_gated_backward_workspace_size(int(n_tok), int(d_col),
+                                                                    int(d_row)))
 
 
 def gptq_debug_arm_wait_probe(kernel: int, limit_ns: int) -> None:

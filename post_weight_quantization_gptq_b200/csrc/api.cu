@@ -101,6 +101,16 @@ bool bad_rows(const uint16_t* p, int64_t ld, int64_t cols) {
     return p == nullptr || ld < cols || !aligned(p, 2);
 }
 
+// A bf16 matrix that the tensor memory accelerator reads: rows of 16-byte units.
+bool bad_tiles(const uint16_t* p, int64_t ld, int64_t cols) {
+    return p == nullptr || ld < cols || (ld % 8) != 0 || !aligned(p, 16);
+}
+
+bool bad_sizes(int64_t n_tok, int64_t d_col, int64_t d_row) {
+    return n_tok <= 0 || n_tok > (int64_t{1} << 24) || d_col <= 0 || d_col > (int64_t{1} << 24) ||
+           d_row <= 0 || d_row > (int64_t{1} << 24);
+}
+
 bool small_ws(const void* ws, size_t have, size_t need) {
     return need > 0 && (ws == nullptr || !aligned(ws, 256) || have < need);
 }
@@ -358,6 +368,151 @@ gptq_status gptq_dequant_matmul_gated(const uint16_t* X, int64_t n_tok, int64_t 
     a.perm = perm; a.d_row = d_row; a.bits = bits; a.group = group_size;
     a.act = activation; a.Y = Y; a.ldy = ldy; a.ws = ws;
     return launch_status(gptq::launch_linear_decode(a, stream));
+}
+
+size_t gptq_dequant_gemm_linear_workspace_size(int64_t n_tok, int64_t d_col, int64_t d_row) {
+    if (bad_sizes(n_tok, d_col, d_row)) return 0;
+    return gptq::linear_gemm_workspace_bytes(n_tok, d_col, d_row, false);
+}
+
+size_t gptq_dequant_gemm_gated_workspace_size(int64_t n_tok, int64_t d_col, int64_t d_row) {
+    if (bad_sizes(n_tok, d_col, d_row)) return 0;
+    return gptq::linear_gemm_workspace_bytes(n_tok, d_col, d_row, true);
+}
+
+size_t gptq_dequant_gemm_linear_backward_workspace_size(int64_t n_tok, int64_t d_col, int64_t d_row) {
+    if (bad_sizes(n_tok, d_col, d_row)) return 0;
+    return gptq::linear_backward_workspace_bytes(n_tok, d_col, d_row, false);
+}
+
+size_t gptq_dequant_gemm_gated_backward_workspace_size(int64_t n_tok, int64_t d_col, int64_t d_row) {
+    if (bad_sizes(n_tok, d_col, d_row)) return 0;
+    return gptq::linear_backward_workspace_bytes(n_tok, d_col, d_row, true);
+}
+
+gptq_status gptq_dequant_gemm_linear(const uint16_t* X, int64_t n_tok, int64_t d_col, int64_t ldx,
+                                     const uint32_t* packed, const float* scales,
+                                     const int32_t* zeros, const int32_t* perm, int64_t d_row,
+                                     int32_t bits, int32_t group_size, const float* bias,
+                                     int32_t activation, const uint16_t* residual, int64_t ldr,
+                                     uint16_t* pre, int64_t ldpre, uint16_t* Y, int64_t ldy,
+                                     int32_t* dev_status, void* ws, size_t ws_bytes,
+                                     cudaStream_t stream) {
+    gptq_status c = check_packed(packed, scales, zeros);
+    if (c == GPTQ_OK) c = check_shape(n_tok, d_col, d_row, bits, group_size, activation, perm);
+    if (c != GPTQ_OK || n_tok == 0) return c;
+    if (bad_rows(X, ldx, d_col) || bad_rows(Y, ldy, d_row)) return GPTQ_ERR_INVALID_ARG;
+    if (residual != nullptr && bad_rows(residual, ldr, d_row)) return GPTQ_ERR_INVALID_ARG;
+    if (pre != nullptr && bad_rows(pre, ldpre, d_row)) return GPTQ_ERR_INVALID_ARG;
+    if (!aligned(bias, 4) || !aligned(dev_status, 4)) return GPTQ_ERR_INVALID_ARG;
+    gptq::LinearCall a = {};
+    a.X = X; a.n_tok = n_tok; a.d_col = d_col; a.ldx = ldx;
+    a.mat[0] = {packed, scales, zeros};
+    a.perm = perm; a.d_row = d_row; a.bits = bits; a.group = group_size;
+    a.bias = bias; a.act = activation; a.residual = residual; a.ldr = ldr;
+    a.pre[0] = pre; a.ldpre[0] = ldpre;
+    a.Y = Y; a.ldy = ldy; a.status = dev_status; a.ws = ws;
+    if (gptq::linear_gemm_needs_workspace(a) &&
+        small_ws(ws, ws_bytes, gptq::linear_gemm_workspace_bytes(n_tok, d_col, d_row, false)))
+        return GPTQ_ERR_WORKSPACE;
+    return launch_status(gptq::launch_linear_gemm(a, stream));
+}
+
+gptq_status gptq_dequant_gemm_gated(const uint16_t* X, int64_t n_tok, int64_t d_col, int64_t ldx,
+                                    const uint32_t* packed_gate, const float* scales_gate,
+                                    const int32_t* zeros_gate, const uint32_t* packed_up,
+                                    const float* scales_up, const int32_t* zeros_up,
+                                    const int32_t* perm, int64_t d_row, int32_t bits,
+                                    int32_t group_size, int32_t activation, uint16_t* gate,
+                                    int64_t ldgate, uint16_t* up, int64_t ldup, uint16_t* Y,
+                                    int64_t ldy, int32_t* dev_status, void* ws, size_t ws_bytes,
+                                    cudaStream_t stream) {
+    gptq_status c = check_packed(packed_gate, scales_gate, zeros_gate);
+    if (c == GPTQ_OK) c = check_packed(packed_up, scales_up, zeros_up);
+    if (c == GPTQ_OK) c = check_shape(n_tok, d_col, d_row, bits, group_size, activation, perm);
+    if (c != GPTQ_OK || n_tok == 0) return c;
+    if (bad_rows(X, ldx, d_col) || bad_rows(Y, ldy, d_row)) return GPTQ_ERR_INVALID_ARG;
+    if (gate != nullptr && bad_rows(gate, ldgate, d_row)) return GPTQ_ERR_INVALID_ARG;
+    if (up != nullptr && bad_rows(up, ldup, d_row)) return GPTQ_ERR_INVALID_ARG;
+    if (!aligned(dev_status, 4)) return GPTQ_ERR_INVALID_ARG;
+    gptq::LinearCall a = {};
+    a.X = X; a.n_tok = n_tok; a.d_col = d_col; a.ldx = ldx;
+    a.mat[0] = {packed_gate, scales_gate, zeros_gate};
+    a.mat[1] = {packed_up, scales_up, zeros_up};
+    a.perm = perm; a.d_row = d_row; a.bits = bits; a.group = group_size; a.act = activation;
+    a.pre[0] = gate; a.ldpre[0] = ldgate;
+    a.pre[1] = up; a.ldpre[1] = ldup;
+    a.Y = Y; a.ldy = ldy; a.status = dev_status; a.ws = ws;
+    if (gptq::linear_gemm_needs_workspace(a) &&
+        small_ws(ws, ws_bytes, gptq::linear_gemm_workspace_bytes(n_tok, d_col, d_row, true)))
+        return GPTQ_ERR_WORKSPACE;
+    return launch_status(gptq::launch_linear_gemm(a, stream));
+}
+
+gptq_status gptq_dequant_gemm_linear_backward(
+    const uint16_t* dY, int64_t n_tok, int64_t d_row, int64_t lddy, const uint32_t* packed,
+    const float* scales, const int32_t* zeros, const int32_t* perm, int64_t d_col, int32_t bits,
+    int32_t group_size, int32_t activation, const uint16_t* pre, int64_t ldpre, uint16_t* dPre,
+    int64_t lddpre, float* dbias, uint16_t* dX, int64_t lddx, int32_t* dev_status, void* ws,
+    size_t ws_bytes, cudaStream_t stream) {
+    gptq_status c = check_packed(packed, scales, zeros);
+    if (c == GPTQ_OK) c = check_shape(n_tok, d_col, d_row, bits, group_size, activation, perm);
+    if (c != GPTQ_OK) return c;
+    if (!aligned(dbias, 4) || !aligned(dev_status, 4)) return GPTQ_ERR_INVALID_ARG;
+    if (n_tok == 0) {   // no tokens: the bias gradient is an empty sum
+        if (dbias != nullptr && cudaMemsetAsync(dbias, 0, d_row * sizeof(float), stream) != cudaSuccess)
+            return GPTQ_ERR_CUDA;
+        return GPTQ_OK;
+    }
+    if (bad_rows(dY, lddy, d_row) || bad_rows(dX, lddx, d_col)) return GPTQ_ERR_INVALID_ARG;
+    // the tensor memory accelerator reads the products' gradient: dPre, or dY itself
+    if (dPre != nullptr ? bad_tiles(dPre, lddpre, d_row)
+                        : (activation != GPTQ_ACT_NONE || bad_tiles(dY, lddy, d_row)))
+        return GPTQ_ERR_INVALID_ARG;
+    if (activation != GPTQ_ACT_NONE && bad_rows(pre, ldpre, d_row)) return GPTQ_ERR_INVALID_ARG;
+    gptq::BackwardCall a = {};
+    a.dY = dY; a.n_tok = n_tok; a.d_row = d_row; a.lddy = lddy;
+    a.mat[0] = {packed, scales, zeros};
+    a.perm = perm; a.d_col = d_col; a.bits = bits; a.group = group_size; a.act = activation;
+    a.pre[0] = pre; a.ldpre[0] = ldpre;
+    a.dP[0] = dPre; a.lddp[0] = lddpre;
+    a.dbias = dbias; a.dX = dX; a.lddx = lddx; a.status = dev_status; a.ws = ws;
+    if (gptq::linear_backward_needs_workspace(a) &&
+        small_ws(ws, ws_bytes, gptq::linear_backward_workspace_bytes(n_tok, d_col, d_row, false)))
+        return GPTQ_ERR_WORKSPACE;
+    return launch_status(gptq::launch_linear_backward(a, stream));
+}
+
+gptq_status gptq_dequant_gemm_gated_backward(
+    const uint16_t* dY, int64_t n_tok, int64_t d_row, int64_t lddy, const uint16_t* gate,
+    int64_t ldgate, const uint16_t* up, int64_t ldup, const uint32_t* packed_gate,
+    const float* scales_gate, const int32_t* zeros_gate, const uint32_t* packed_up,
+    const float* scales_up, const int32_t* zeros_up, const int32_t* perm, int64_t d_col,
+    int32_t bits, int32_t group_size, int32_t activation, uint16_t* dGate, int64_t lddgate,
+    uint16_t* dUp, int64_t lddup, uint16_t* dX, int64_t lddx, int32_t* dev_status, void* ws,
+    size_t ws_bytes, cudaStream_t stream) {
+    gptq_status c = check_packed(packed_gate, scales_gate, zeros_gate);
+    if (c == GPTQ_OK) c = check_packed(packed_up, scales_up, zeros_up);
+    if (c == GPTQ_OK) c = check_shape(n_tok, d_col, d_row, bits, group_size, activation, perm);
+    if (c != GPTQ_OK || n_tok == 0) return c;
+    if (bad_rows(dY, lddy, d_row) || bad_rows(gate, ldgate, d_row) || bad_rows(up, ldup, d_row) ||
+        bad_rows(dX, lddx, d_col) || bad_tiles(dGate, lddgate, d_row) || bad_tiles(dUp, lddup, d_row))
+        return GPTQ_ERR_INVALID_ARG;
+    if (dGate == dUp || !aligned(dev_status, 4)) return GPTQ_ERR_INVALID_ARG;
+    gptq::BackwardCall a = {};
+    a.dY = dY; a.n_tok = n_tok; a.d_row = d_row; a.lddy = lddy;
+    a.mat[0] = {packed_gate, scales_gate, zeros_gate};
+    a.mat[1] = {packed_up, scales_up, zeros_up};
+    a.perm = perm; a.d_col = d_col; a.bits = bits; a.group = group_size; a.act = activation;
+    a.pre[0] = gate; a.ldpre[0] = ldgate;
+    a.pre[1] = up; a.ldpre[1] = ldup;
+    a.dP[0] = dGate; a.lddp[0] = lddgate;
+    a.dP[1] = dUp; a.lddp[1] = lddup;
+    a.dX = dX; a.lddx = lddx; a.status = dev_status; a.ws = ws;
+    if (gptq::linear_backward_needs_workspace(a) &&
+        small_ws(ws, ws_bytes, gptq::linear_backward_workspace_bytes(n_tok, d_col, d_row, true)))
+        return GPTQ_ERR_WORKSPACE;
+    return launch_status(gptq::launch_linear_backward(a, stream));
 }
 
 gptq_status gptq_sync_status(cudaStream_t stream, const int32_t* dev_status, int32_t* out) {

@@ -475,6 +475,11 @@ cudaError_t launch_bits(const CUtensorMap& ta, const CUtensorMap& tp, const floa
 
 }  // namespace
 
+cudaError_t launch_gather_bf16(const uint16_t* X, int64_t ldx, int64_t n_tok, int d_col,
+                               const int32_t* perm, uint16_t* Xq, cudaStream_t stream) {
+    return launch_gather(X, ldx, n_tok, d_col, perm, Xq, stream);
+}
+
 size_t dequant_gemm_workspace_bytes(int64_t n_tok, int64_t d_col) {
     return ((static_cast<size_t>(n_tok) * d_col * 2 + 255) / 256) * 256;
 }

@@ -143,6 +143,41 @@ inline bool needs_gather(const uint16_t* X, int64_t ldx, const int32_t* perm) {
 size_t linear_decode_workspace_bytes(int64_t n_tok, int64_t d_col);
 gptq_status launch_linear_decode(const LinearCall& c, cudaStream_t stream);
 
+// ---- many-token form (linear_gemm.cu)
+cudaError_t launch_gather_bf16(const uint16_t* X, int64_t ldx, int64_t n_tok, int d_col,
+                               const int32_t* perm, uint16_t* Xq, cudaStream_t stream);
+size_t linear_gemm_workspace_bytes(int64_t n_tok, int64_t d_col, int64_t d_row, bool gated);
+bool linear_gemm_needs_workspace(const LinearCall& c);
+gptq_status launch_linear_gemm(const LinearCall& c, cudaStream_t stream);
+
+// ---- gradients (linear_backward.cu: slopes, bias sums and the column order;
+// linear_gemm.cu: the product).  mat[1], pre[1] and dP[1] are given by the
+// gated form only; dP[0] may be NULL for a linear layer without activation.
+struct BackwardCall {
+    const uint16_t* dY;
+    int64_t n_tok, d_row, lddy;
+    PackedMatrix mat[2];
+    const int32_t* perm;
+    int64_t d_col;
+    int bits, group, act;
+    const uint16_t* pre[2];
+    int64_t ldpre[2];
+    uint16_t* dP[2];
+    int64_t lddp[2];
+    float* dbias;
+    uint16_t* dX;
+    int64_t lddx;
+    int32_t* status;
+    void* ws;
+};
+size_t bias_partial_bytes(int64_t n_tok, int64_t d_row);
+gptq_status launch_slopes(const BackwardCall& c, float* bias_part, int64_t* launches, cudaStream_t stream);
+gptq_status launch_scatter(const uint16_t* dXq, int64_t n_tok, int d_col, const int32_t* perm, uint16_t* dX,
+                           int64_t lddx, cudaStream_t stream);
+size_t linear_backward_workspace_bytes(int64_t n_tok, int64_t d_col, int64_t d_row, bool gated);
+bool linear_backward_needs_workspace(const BackwardCall& c);
+gptq_status launch_linear_backward(const BackwardCall& c, cudaStream_t stream);
+
 // ---- stage 5 (pack.cu)
 gptq_status launch_pack(const uint8_t* codes, int64_t d_row, int64_t d_col, int bits,
                         uint32_t* packed, cudaStream_t stream);

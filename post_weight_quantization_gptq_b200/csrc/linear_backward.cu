@@ -1,0 +1,220 @@
+// What surrounds the gradient product of the layers with an epilogue:
+//   slopes   linear  dP = dY * act'(pre),  dbias[n] = sum_t dP[t][n]
+//            gated   dG = dY * U * act'(G),  dU = dY * act(G)
+//            in fp32 from the saved bf16 pre-activations, rounded to bf16 once
+//            (the tensor cores read them as 16-bit operands); the bias sums
+//            take the unrounded values.
+//   scatter  dX[t][perm[k]] = dXq[t][k], a token row at a time through shared
+//            memory, so that HBM sees rows in order on both sides.
+// Both are bound by HBM: every value is read and written once.  Bias sums are
+// two-step (token slabs, then slabs in order) instead of atomic adds, so that
+// they have the same bits every call.
+#include "activation.cuh"
+#include "common.cuh"
+#include "kernels.h"
+
+namespace gptq {
+namespace {
+
+constexpr int kCols = 256;      // columns per CTA: 32 lanes x 8
+constexpr int kRows = 8;        // token rows in flight per CTA
+constexpr int kMaxSlabs = 256;  // token slabs of the bias sums
+
+// Tokens per CTA: 32, or as many as leave at most kMaxSlabs slabs.
+int64_t slab_tokens(int64_t n_tok) {
+    const int64_t least = (n_tok + kMaxSlabs - 1) / kMaxSlabs;
+    return least <= 32 ? 32 : (least + kRows - 1) / kRows * kRows;
+}
+int64_t slabs(int64_t n_tok) { return (n_tok + slab_tokens(n_tok) - 1) / slab_tokens(n_tok); }
+
+__device__ __forceinline__ void get8(const uint16_t* p, float (&v)[8], int count) {
+    if (count == 8 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+        const uint4 q = *reinterpret_cast<const uint4*>(p);
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[2 * j] = __uint_as_float(w[j] << 16);
+            v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = j < count ? bf16_to_float(p[j]) : 0.f;
+    }
+}
+// dP rows start on 16 bytes and c is a multiple of 8
+__device__ __forceinline__ void put8(uint16_t* p, const float (&v)[8], int count) {
+    if (count == 8) {
+        *reinterpret_cast<uint4*>(p) = make_uint4(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]),
+                                                  f32x2_to_bf16x2(v[4], v[5]), f32x2_to_bf16x2(v[6], v[7]));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < count) p[j] = f32_to_bf16_bits(v[j]);
+    }
+}
+
+// The outputs may be the inputs themselves: a thread reads its eight entries
+// of all of them before it writes.
+template <bool GATED>
+__global__ void __launch_bounds__(256) slopes_kernel(const BackwardCall c, float* bias_part, int64_t slab) {
+    __shared__ float sums[kRows][kCols + 8];
+    const int lane = threadIdx.x & 31, r = threadIdx.x >> 5;
+    const int64_t n = blockIdx.x * static_cast<int64_t>(kCols) + 8 * lane;
+    const int count = static_cast<int>(c.d_row - n < 8 ? c.d_row - n : 8);
+    const int64_t t1 = (blockIdx.y + 1) * slab < c.n_tok ? (blockIdx.y + 1) * slab : c.n_tok;
+    float sum[8] = {};
+    if (count > 0) {
+#pragma unroll 2
+        for (int64_t t = blockIdx.y * slab + r; t < t1; t += kRows) {
+            float dy[8];
+            get8(c.dY + t * c.lddy + n, dy, count);
+            if constexpr (GATED) {
+                float g[8], u[8];
+                get8(c.pre[0] + t * c.ldpre[0] + n, g, count);
+                get8(c.pre[1] + t * c.ldpre[1] + n, u, count);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    u[j] = dy[j] * u[j] * activate_slope(g[j], c.act);
+                    g[j] = dy[j] * activate(g[j], c.act);
+                }
+                put8(c.dP[0] + t * c.lddp[0] + n, u, count);
+                put8(c.dP[1] + t * c.lddp[1] + n, g, count);
+            } else {
+                if (c.act != GPTQ_ACT_NONE) {
+                    float p[8];
+                    get8(c.pre[0] + t * c.ldpre[0] + n, p, count);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) dy[j] *= activate_slope(p[j], c.act);
+                }
+                if (c.dP[0] != nullptr) put8(c.dP[0] + t * c.lddp[0] + n, dy, count);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum[j] += dy[j];
+            }
+        }
+    }
+    if constexpr (!GATED) {
+        if (bias_part == nullptr) return;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sums[r][8 * lane + j] = sum[j];
+        __syncthreads();
+        const int64_t col = blockIdx.x * static_cast<int64_t>(kCols) + threadIdx.x;
+        if (col < c.d_row) {
+            float v = 0.f;
+#pragma unroll
+            for (int q = 0; q < kRows; ++q) v += sums[q][threadIdx.x];
+            bias_part[blockIdx.y * c.d_row + col] = v;
+        }
+    }
+}
+
+__global__ void __launch_bounds__(256) bias_sum_kernel(const float* __restrict__ part, int slabs, int64_t d_row,
+                                                       float* __restrict__ dbias) {
+    const int64_t n = blockIdx.x * 256ll + threadIdx.x;
+    if (n >= d_row) return;
+    float v[4] = {};   // four chains, joined in a fixed order
+    for (int s = 0; s < slabs; s += 4)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (s + q < slabs) v[q] += part[(s + q) * d_row + n];
+    dbias[n] = (v[0] + v[1]) + (v[2] + v[3]);
+}
+
+constexpr int kScatterThreads = 512;
+constexpr int kScatterSmem = 220 * 1024;
+
+// One token row at a time: its values go to their columns in shared memory and
+// leave in order.  The permutation is staged once per CTA as 16-bit indices
+// (kSmall: d_col <= 65536 and both fit), entries outside [0, d_col) read as k.
+template <bool kSmall>
+__global__ void __launch_bounds__(kScatterThreads) scatter_kernel(const uint16_t* __restrict__ dXq, int64_t n_tok,
+                                                                  int K, const int32_t* __restrict__ perm,
+                                                                  uint16_t* __restrict__ dX, int64_t lddx) {
+    extern __shared__ __align__(16) uint16_t sm[];
+    if constexpr (!kSmall) {
+        for (int64_t t = blockIdx.x; t < n_tok; t += gridDim.x)
+            for (int k = threadIdx.x; k < K; k += kScatterThreads) {
+                int col = __ldg(perm + k);
+                if (col < 0 || col >= K) col = k;
+                dX[t * lddx + col] = dXq[t * K + k];
+            }
+        return;
+    }
+    uint16_t* idx = sm;        // [K]
+    uint16_t* row = sm + K;    // [K]
+    for (int k = threadIdx.x; k < K; k += kScatterThreads) {
+        int col = perm[k];
+        if (col < 0 || col >= K) col = k;
+        idx[k] = static_cast<uint16_t>(col);
+        row[k] = 0;
+    }
+    const int chunks = K / 8;
+    for (int64_t t = blockIdx.x; t < n_tok; t += gridDim.x) {
+        __syncthreads();   // the row buffer has been written out (first: idx is there)
+        const uint4* src = reinterpret_cast<const uint4*>(dXq + t * K);
+        for (int c = threadIdx.x; c < chunks; c += kScatterThreads) {
+            const uint4 v = src[c], ix = reinterpret_cast<const uint4*>(idx)[c];
+            const uint32_t vw[4] = {v.x, v.y, v.z, v.w}, iw[4] = {ix.x, ix.y, ix.z, ix.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                row[iw[j] & 0xFFFFu] = static_cast<uint16_t>(vw[j]);
+                row[iw[j] >> 16] = static_cast<uint16_t>(vw[j] >> 16);
+            }
+        }
+        __syncthreads();
+        uint16_t* out = dX + t * lddx;
+        if ((reinterpret_cast<uintptr_t>(out) & 15) == 0) {
+            for (int c = threadIdx.x; c < chunks; c += kScatterThreads)
+                reinterpret_cast<uint4*>(out)[c] = reinterpret_cast<const uint4*>(row)[c];
+        } else {
+            for (int k = threadIdx.x; k < K; k += kScatterThreads) out[k] = row[k];
+        }
+    }
+}
+
+}  // namespace
+
+size_t bias_partial_bytes(int64_t n_tok, int64_t d_row) {
+    return static_cast<size_t>(slabs(n_tok)) * d_row * sizeof(float);
+}
+
+gptq_status launch_slopes(const BackwardCall& c, float* bias_part, int64_t* launches, cudaStream_t stream) {
+    const bool gated = c.mat[1].packed != nullptr;
+    if (!gated && c.dP[0] == nullptr && bias_part == nullptr) return GPTQ_OK;   // dY is the gradient
+    const int64_t ns = slabs(c.n_tok);
+    const dim3 grid(static_cast<unsigned>((c.d_row + kCols - 1) / kCols), static_cast<unsigned>(ns));
+    if (gated) slopes_kernel<true><<<grid, 256, 0, stream>>>(c, nullptr, slab_tokens(c.n_tok));
+    else slopes_kernel<false><<<grid, 256, 0, stream>>>(c, bias_part, slab_tokens(c.n_tok));
+    if (cudaGetLastError() != cudaSuccess) return GPTQ_ERR_CUDA;
+    ++*launches;
+    if (bias_part != nullptr) {
+        bias_sum_kernel<<<static_cast<unsigned>((c.d_row + 255) / 256), 256, 0, stream>>>(
+            bias_part, static_cast<int>(ns), c.d_row, c.dbias);
+        if (cudaGetLastError() != cudaSuccess) return GPTQ_ERR_CUDA;
+        ++*launches;
+    }
+    return GPTQ_OK;
+}
+
+gptq_status launch_scatter(const uint16_t* dXq, int64_t n_tok, int d_col, const int32_t* perm, uint16_t* dX,
+                           int64_t lddx, cudaStream_t stream) {
+    const size_t smem = static_cast<size_t>(d_col) * 4;
+    if (d_col <= 65536 && smem <= kScatterSmem) {
+        auto kern = scatter_kernel<true>;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
+            cudaSuccess)
+            return GPTQ_ERR_CUDA;
+        int per_sm = 0;
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kScatterThreads, smem) != cudaSuccess)
+            return GPTQ_ERR_CUDA;
+        const int64_t resident = static_cast<int64_t>(per_sm > 0 ? per_sm : 1) * num_sms();
+        kern<<<static_cast<int>(n_tok < resident ? n_tok : resident), kScatterThreads, smem, stream>>>(
+            dXq, n_tok, d_col, perm, dX, lddx);
+    } else {
+        const int64_t want = 4 * num_sms();
+        scatter_kernel<false><<<static_cast<int>(n_tok < want ? n_tok : want), kScatterThreads, 0, stream>>>(
+            dXq, n_tok, d_col, perm, dX, lddx);
+    }
+    return cudaGetLastError() == cudaSuccess ? GPTQ_OK : GPTQ_ERR_CUDA;
+}
+
+}  // namespace gptq

@@ -1,0 +1,797 @@
+// Many tokens through packed layers on the 5th-generation tensor cores, with
+// the epilogue of the layer, and the gradient with respect to the tokens:
+//   linear    Y = act(Xq W^T + bias) + residual          (Xq[t][k] = X[t][perm[k]])
+//   gated     Y = act(Xq Wg^T) * (Xq Wu^T)
+//   backward  dXq = dP W  (linear),  dXq = dG Wg + dU Wu  (gated)
+// with the 16-bit weights W[n][k] = bf16( fp32(s[k/g][n]) * (q[n][k] - z[k/g][n]) ):
+// products of two bf16 values are exact, sums are fp32, outputs are rounded to
+// bf16 once.
+//
+// One kernel for the three.  A CTA owns a tile of 256 tokens x 256 columns (two
+// 128 x 256 accumulators, all of tensor memory) and sweeps the contraction in
+// stages of 64:
+//   warp 0      TMA: the stage's tokens (2 x 128 x 64 bf16, 128-byte swizzle)
+//   warp 10     TMA: the stage's packed words, in a ring of their own
+//   warp 1      tensor memory and the MMAs (kind::f16, M 128, N 256, K 16)
+//   warps 2..9  dequantize the stage's 256 x 64 weights into a bf16 tile in
+//               shared memory, one thread per 64 codes of one weight row; after
+//               the sweep they drain the accumulators through the epilogue
+// linear    the tile's columns are 256 weight rows n, the stage 64 of their k:
+//           the weight tile is K-major.
+// gated     the columns are 128 rows of the gate and the same 128 of the up
+//           matrix, so a thread finds both products of an output in its own
+//           tensor-memory lane and the gate product never leaves the chip.
+// backward  the columns are 256 k, the stage 64 weight rows n: a thread still
+//           writes 64 codes of one row as 128 bytes, which now is the MN-major
+//           layout of the same tile; the two matrices of the gated form are two
+//           sweeps into one accumulator.
+// A thread looks its weights up: the 2^bits weights of a group are computed
+// once (8 instructions per 4 of them), kept as bytes in registers and picked
+// by byte permutes, 3 instructions per 4-bit code, so that 16,384 codes per
+// stage take about half of the 1024 cycles of the stage's MMAs; 8-bit codes are
+// computed one by one.  A tile whose second 128 tokens lie past the end skips
+// that half's loads and MMAs.
+//
+// Tiles that do not fill the last wave of SMs split the contraction: their
+// partial tiles go to the workspace and a second kernel adds them in order and
+// runs the epilogue.  No atomics: same bits every call.  Every wait is bounded
+// (GPTQ_ERR_TIMEOUT).
+#include <cuda.h>
+
+#include "activation.cuh"
+#include "common.cuh"
+#include "dequant.cuh"
+#include "kernels.h"
+
+namespace gptq {
+namespace {
+
+enum Mode { kLinear, kGated, kBack };
+
+constexpr int TM = 256;                       // tokens per tile (two halves)
+constexpr int TN = 256;                       // tile columns (MMA N)
+constexpr int BK = 64;                        // contraction per stage
+constexpr int kAStages = 3;
+constexpr int kHalfBytes = 128 * BK * 2;      // 16 KB: one half's tokens
+constexpr int kABytes = 2 * kHalfBytes;
+constexpr int kBBytes = TN * BK * 2;          // 32 KB: one dequantized tile
+constexpr int kMaxBBufs = 3, kMaxPStages = 6;
+constexpr int kThreads = 352;
+constexpr uint32_t kTmemCols = 512;
+constexpr int kSms = 148;                     // SMs of the device this library is built for
+constexpr int kMinStages = 8;                 // least stages of a split tile's part
+constexpr int kMaxSplit = 16;
+
+// Packed words of a stage.  A box of the tensor map is 64 codes wide (16 bytes
+// or more) except at 3 bits, where 64 codes are 24 bytes: its boxes hold 128
+// codes, two stages of the forward sweep.
+template <int BITS, int MODE>
+struct Geom {
+    static constexpr int kBoxCodes = BITS == 3 ? 128 : 64;
+    static constexpr int kBoxWords = kBoxCodes * BITS / 32;
+    static constexpr int kRowBytes = kBoxWords * 4;
+    static constexpr bool kPairs = BITS == 3 && MODE != kBack;   // a slot serves two stages
+    static constexpr int kSlot = MODE == kBack ? 64 * TN * BITS / 8 : TN * kRowBytes;
+    static constexpr int kPStages = BITS == 8 ? 3 : BITS == 4 ? 4 : BITS == 3 ? 2 : 6;
+    static constexpr int kBBufs = BITS == 8 ? 2 : 3;
+    static constexpr int kSmem = kAStages * kABytes + kBBufs * kBBytes + kPStages * kSlot + 1024 + 256;
+};
+
+struct Bars {
+    uint64_t afull[kAStages], aempty[kAStages];
+    uint64_t pfull[kMaxPStages], pempty[kMaxPStages];
+    uint64_t bfull[kMaxBBufs], bempty[kMaxBBufs];
+    uint64_t acc_full, drain;
+    uint32_t tmem;
+    int abort;
+};
+
+struct Args {
+    PackedMatrix mat[2];
+    int n_tok, N;        // rows and columns of the output
+    int nk;              // stages of the whole contraction
+    int nk1;             // backward: stages of the first matrix
+    int d_row, d_col, g;
+    int tiles_n, tiles_t;
+    int full, split, per;   // whole tiles; parts of the others and their stages
+    int part_rows;          // tokens of a partial tile
+    float* part;
+    const float* bias;
+    int act;
+    const uint16_t* residual;
+    int64_t ldr;
+    uint16_t* pre[2];
+    int64_t ldpre[2];
+    uint16_t* Y;
+    int64_t ldy;
+    int32_t* status;
+};
+
+// ------------------------------------------------------------- epilogue
+__device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8], int count) {
+    if (count == 8 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+        *reinterpret_cast<uint4*>(p) = make_uint4(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]),
+                                                  f32x2_to_bf16x2(v[4], v[5]), f32x2_to_bf16x2(v[6], v[7]));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < count) p[j] = f32_to_bf16_bits(v[j]);
+    }
+}
+__device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8], int count) {
+    if (count == 8 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+        const uint4 q = *reinterpret_cast<const uint4*>(p);
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[2 * j] = __uint_as_float(w[j] << 16);
+            v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = j < count ? bf16_to_float(p[j]) : 0.f;
+    }
+}
+
+// Eight consecutive outputs of token t from column n on: v their sums (gated:
+// of the gate, u of the up matrix).
+template <int MODE>
+__device__ __forceinline__ void emit8(const Args& a, int t, int n, float (&v)[8], const float (&u)[8]) {
+    const int count = min(8, a.N - n);
+    if (count <= 0) return;
+    if constexpr (MODE == kLinear) {
+        if (a.bias != nullptr) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < count) v[j] += __ldg(a.bias + n + j);
+        }
+        if (a.pre[0] != nullptr) store8(a.pre[0] + t * a.ldpre[0] + n, v, count);
+        if (a.act != GPTQ_ACT_NONE) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = activate(v[j], a.act);
+        }
+        if (a.residual != nullptr) {
+            float r[8];
+            load8(a.residual + t * a.ldr + n, r, count);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] += r[j];
+        }
+    } else if constexpr (MODE == kGated) {
+        if (a.pre[0] != nullptr) store8(a.pre[0] + t * a.ldpre[0] + n, v, count);
+        if (a.pre[1] != nullptr) store8(a.pre[1] + t * a.ldpre[1] + n, u, count);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = activate(v[j], a.act) * u[j];
+    }
+    store8(a.Y + t * a.ldy + n, v, count);
+}
+
+// ------------------------------------------------------- dequantization
+// The 64 packed codes of a thread's stage as words.
+template <int BITS>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[2 * BITS]) {
+    if constexpr (BITS == 3) {
+#pragma unroll
+        for (int q = 0; q < 3; ++q) {
+            const uint2 v = reinterpret_cast<const uint2*>(p)[q];
+            w[2 * q] = v.x;
+            w[2 * q + 1] = v.y;
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < BITS / 2; ++q) {
+            const uint4 v = reinterpret_cast<const uint4*>(p)[q];
+            w[4 * q] = v.x; w[4 * q + 1] = v.y; w[4 * q + 2] = v.z; w[4 * q + 3] = v.w;
+        }
+    }
+}
+
+// The 2^BITS weights of a group, bf16(s (q - z)), as byte tables: entry 4j + i
+// has its low byte in byte i of lo[j] and its high byte in byte i of hi[j].
+template <int BITS>
+struct Table {
+    static constexpr int W = (1 << BITS) / 4;
+    uint32_t lo[W], hi[W];
+};
+template <int BITS>
+__device__ __forceinline__ void build_table(float s, float z, Table<BITS>& tab) {
+    const uint64_t s2 = pk2(s, s), z2 = pk2(z, z);
+#pragma unroll
+    for (int j = 0; j < Table<BITS>::W; ++j) {
+        uint32_t r[2];
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const float q0 = static_cast<float>(4 * j + 2 * p);
+            const uint64_t v = mul2(sub2(pk2(q0, q0 + 1.f), z2), s2);  // q - z exact, one rounding
+            float lo, hi;
+            asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+            r[p] = f32x2_to_bf16x2(lo, hi);
+        }
+        tab.lo[j] = __byte_perm(r[0], r[1], 0x6420);
+        tab.hi[j] = __byte_perm(r[0], r[1], 0x7531);
+    }
+}
+
+// Codes 8c .. 8c+7 of the words as four bf16x2 weights.  Two and three bits: the
+// codes spread to one per nibble select among the table's bytes directly.
+template <int BITS>
+__device__ __forceinline__ void lookup(const uint32_t (&w)[2 * BITS], int c, const Table<BITS>& tab,
+                                       uint32_t (&o)[4]) {
+    if constexpr (BITS == 4) {
+        lookup8(w[c], tab.lo, tab.hi, o);
+    } else {
+        uint32_t sel;
+        if constexpr (BITS == 3) {
+            const int b = (24 * c) >> 5, sh = (24 * c) & 31;
+            const uint32_t v = sh <= 8 ? (w[b] >> sh) : __funnelshift_r(w[b], w[b + 1 < 6 ? b + 1 : 5], sh);
+            const uint32_t u = (v & 0xFFFu) | ((v & 0xFFF000u) << 4);   // codes 0..3 | 4..7
+            sel = (u & 0x00070007u) | ((u << 1) & 0x00700070u) | ((u << 2) & 0x07000700u) |
+                  ((u << 3) & 0x70007000u);
+        } else {
+            uint32_t v = __byte_perm(w[c >> 1], 0, (c & 1) ? 0x4342 : 0x4140);  // codes 0..3 | 4..7
+            v = (v | (v << 4)) & 0x0F0F0F0Fu;
+            sel = (v | (v << 2)) & 0x33333333u;
+        }
+        const uint32_t l1 = BITS == 3 ? tab.lo[Table<BITS>::W - 1] : 0, h1 = BITS == 3 ? tab.hi[Table<BITS>::W - 1] : 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t s4 = (sel >> (16 * h)) & 0xFFFFu;
+            const uint32_t L = prmt(tab.lo[0], l1, s4), H = prmt(tab.hi[0], h1, s4);
+            o[2 * h] = __byte_perm(L, H, 0x5140);
+            o[2 * h + 1] = __byte_perm(L, H, 0x7362);
+        }
+    }
+}
+
+// Eight 8-bit codes directly: 2^23 + q less 2^23 + z is q - z exactly.
+__device__ __forceinline__ void direct8(const uint32_t (&w)[16], int c, uint64_t s2, uint64_t off2,
+                                        uint32_t (&o)[4]) {
+    float f[8];
+    chunk_codes<8>(w, c, f);
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        const uint64_t v = mul2(sub2(pk2(f[2 * p], f[2 * p + 1]), off2), s2);
+        if (p & 1) {   // the conversion pipe takes half, the fp32 pipe the other half
+            float lo, hi;
+            asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+            o[p] = f32x2_to_bf16x2(lo, hi);
+        } else {
+            o[p] = bf16x2_rne(v);
+        }
+    }
+}
+
+// GPS: groups per 64 codes (1 where g is a multiple of 64 or one group spans the row).
+template <int BITS, int GPS, int MODE>
+__global__ void __launch_bounds__(kThreads, 1)
+    packed_gemm_kernel(const __grid_constant__ CUtensorMap tma0, const __grid_constant__ CUtensorMap tma1,
+                       const __grid_constant__ CUtensorMap tmp0, const __grid_constant__ CUtensorMap tmp1,
+                       const __grid_constant__ Args a) {
+    using G = Geom<BITS, MODE>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    uint8_t* bbuf = smem + kAStages * kABytes;
+    uint8_t* pbuf = bbuf + G::kBBufs * kBBytes;
+    Bars* bars = reinterpret_cast<Bars*>(pbuf + G::kPStages * G::kSlot);
+    volatile int* abort = &bars->abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    // this CTA's tile and its part of the contraction
+    int tile = blockIdx.x, k0 = 0, k1 = a.nk, slot = -1;
+    if (tile >= a.full) {
+        slot = tile - a.full;
+        tile = a.full + slot / a.split;
+        k0 = (slot % a.split) * a.per;
+        k1 = min(a.nk, k0 + a.per);
+    }
+    const int t0 = (tile / a.tiles_n) * TM;
+    const int n0 = (tile % a.tiles_n) * (MODE == kGated ? TN / 2 : TN);
+    const int halves = t0 + 128 < a.n_tok ? 2 : 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kAStages; ++s) {
+            mbar_init(&bars->afull[s], 1);
+            mbar_init(&bars->aempty[s], 1);
+        }
+        for (int s = 0; s < G::kPStages; ++s) {
+            mbar_init(&bars->pfull[s], 1);
+            mbar_init(&bars->pempty[s], 256);
+        }
+        for (int b = 0; b < G::kBBufs; ++b) {
+            mbar_init(&bars->bfull[b], 256);
+            mbar_init(&bars->bempty[b], 1);
+        }
+        mbar_init(&bars->acc_full, 1);
+        mbar_init(&bars->drain, 1);
+        bars->abort = 0;
+        fence_barrier_init();
+        tma_prefetch_desc(&tma0);
+        tma_prefetch_desc(&tmp0);
+    }
+    if (warp == 1) {
+        tmem_alloc(&bars->tmem, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem;
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA: tokens
+        if (lane == 0) {
+            int i = 0;
+            for (int it = k0; it < k1 && !*abort; ++it, ++i) {
+                const int st = i % kAStages;
+                if (!mbar_wait(&bars->aempty[st], ((i / kAStages) & 1u) ^ 1u, abort)) break;
+                const bool second = MODE == kBack && it >= a.nk1;
+                const CUtensorMap* map = second ? &tma1 : &tma0;
+                const int x = (second ? it - a.nk1 : it) * BK;
+                mbar_arrive_expect_tx(&bars->afull[st], halves * kHalfBytes);
+                for (int h = 0; h < halves; ++h)
+                    tma_load_2d(smem + st * kABytes + h * kHalfBytes, map, &bars->afull[st], x, t0 + 128 * h);
+            }
+            // never leave with copies in flight (bounded even when aborting)
+            volatile int no_abort = 0;
+            for (int j = 0; j < min(i, kAStages); ++j) {
+                const int i2 = i - 1 - j;
+                if (!mbar_wait(&bars->afull[i2 % kAStages], (i2 / kAStages) & 1u, &no_abort)) {
+                    *abort = 1;
+                    break;
+                }
+            }
+        }
+    } else if (warp == 10) {
+        // ------------------------------------------------ TMA: packed words
+        if (lane == 0) {
+            constexpr int kStep = G::kPairs ? 2 : 1;
+            int i = 0;
+            for (int it = k0; it < k1 && !*abort; it += kStep, ++i) {
+                const int ps = i % G::kPStages;
+                if (!mbar_wait(&bars->pempty[ps], ((i / G::kPStages) & 1u) ^ 1u, abort)) break;
+                uint8_t* dst = pbuf + ps * G::kSlot;
+                mbar_arrive_expect_tx(&bars->pfull[ps], G::kSlot);
+                if constexpr (MODE == kBack) {
+                    const bool second = it >= a.nk1;
+                    const int row = (second ? it - a.nk1 : it) * BK;
+                    constexpr int kBoxes = TN / G::kBoxCodes;
+                    for (int c = 0; c < kBoxes; ++c)
+                        tma_load_2d(dst + c * (BK * G::kRowBytes), second ? &tmp1 : &tmp0, &bars->pfull[ps],
+                                    (n0 / G::kBoxCodes + c) * G::kBoxWords, row);
+                } else {
+                    const int x = (it / kStep) * G::kBoxWords;
+                    tma_load_2d(dst, &tmp0, &bars->pfull[ps], x, n0);
+                    tma_load_2d(dst + 128 * G::kRowBytes, MODE == kGated ? &tmp1 : &tmp0, &bars->pfull[ps], x,
+                                MODE == kGated ? n0 : n0 + 128);
+                }
+            }
+            volatile int no_abort = 0;
+            for (int j = 0; j < min(i, G::kPStages); ++j) {
+                const int i2 = i - 1 - j;
+                if (!mbar_wait(&bars->pfull[i2 % G::kPStages], (i2 / G::kPStages) & 1u, &no_abort)) {
+                    *abort = 1;
+                    break;
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            constexpr uint32_t kIdesc = instr_desc(/*bf16*/ 1, /*A K-major*/ 0, /*B*/ MODE == kBack ? 1 : 0, 128, TN);
+            bool ok = true;
+            for (int i = 0; i < k1 - k0; ++i) {
+                const int st = i % kAStages, b = i % G::kBBufs;
+                if (!mbar_wait(&bars->afull[st], (i / kAStages) & 1u, abort) ||
+                    !mbar_wait(&bars->bfull[b], (i / G::kBBufs) & 1u, abort)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t am = smem_u32(smem + st * kABytes);
+                const uint32_t bm = smem_u32(bbuf + b * kBBytes);
+                for (int h = 0; h < halves; ++h)
+#pragma unroll
+                    for (int kk = 0; kk < BK / 16; ++kk) {
+                        // K-major: 32 bytes of each row; MN-major: two atoms of 8
+                        // weight rows, boxes of 64 columns 8 KB apart
+                        const uint64_t bd = MODE == kBack ? smem_desc(bm + kk * 2048, 8192, 1024, 2)
+                                                          : smem_desc(bm + kk * 32, 16, 1024, 2);
+                        mma_f16_ss(tmem + h * TN, smem_desc(am + h * kHalfBytes + kk * 32, 16, 1024, 2), bd, kIdesc,
+                                   (i > 0 || kk > 0) ? 1u : 0u);
+                    }
+                mma_commit(&bars->aempty[st]);
+                mma_commit(&bars->bempty[b]);
+            }
+            if (ok) mma_commit(&bars->acc_full);
+            mma_commit(&bars->drain);
+            volatile int no_abort = 0;
+            if (!mbar_wait(&bars->drain, 0, &no_abort)) *abort = 1;
+        }
+    } else {
+        // ------------------------------------------------ dequantize
+        const int j = threadIdx.x - 64;   // 0..255: the thread's 128 bytes of the weight tile
+        // forward: weight row `wrow` of matrix `mi`; backward: row 64 it + (j & 63),
+        // columns n0 + 64 (j >> 6) on
+        const int mi = MODE == kGated ? j >> 7 : 0;
+        const int wrow = n0 + (MODE == kGated ? (j & 127) : j);
+        const int kcol = n0 + 64 * (j >> 6);
+        const int groups = (a.d_col + a.g - 1) / a.g;
+        float s[GPS] = {}, z[GPS] = {}, s_nx[GPS], z_nx[GPS];
+        auto pair = [&](const PackedMatrix& m, int gi, int row, bool in, float& sv, float& zv) {
+            sv = 0.f;   // rows and columns past the layer: weights 0
+            zv = 0.f;
+            if (in) {
+                const int64_t at = static_cast<int64_t>(gi) * a.d_row + row;
+                sv = __ldg(m.scales + at);
+                zv = static_cast<float>(__ldg(m.zeros + at));
+            }
+        };
+        // the scales of stage `it` (forward with GPS 1: of group `it`)
+        auto fetch = [&](int it) {
+#pragma unroll
+            for (int q = 0; q < GPS; ++q) {
+                if constexpr (MODE == kBack) {
+                    const bool second = it >= a.nk1;
+                    const int row = (second ? it - a.nk1 : it) * BK + (j & 63);
+                    const int gi = GPS == 1 ? kcol / a.g : (kcol / 64) * GPS + q;
+                    pair(a.mat[second ? 1 : 0], gi, row, it < k1 && row < a.d_row && kcol < a.d_col, s_nx[q], z_nx[q]);
+                } else {
+                    const int gi = it * GPS + q;
+                    pair(a.mat[mi], gi, wrow, wrow < a.d_row && gi < groups, s_nx[q], z_nx[q]);
+                }
+            }
+        };
+        constexpr bool kByGroup = MODE != kBack && GPS == 1;   // parameters change only with the group
+        int cur_g = kByGroup ? k0 * BK / a.g : 0;
+        int next_start = k0 * BK;                              // kByGroup: where group cur_g takes over
+        fetch(kByGroup ? cur_g : k0);
+        constexpr bool kTable = BITS != 8;
+        Table<BITS == 8 ? 2 : BITS> tab;
+        uint64_t s2 = 0, off2 = 0;
+        auto set = [&](int q) {
+            if constexpr (kTable) {
+                build_table<BITS>(s[q], z[q], tab);
+            } else {
+                s2 = pk2(s[q], s[q]);
+                const float off = 8388608.f + z[q];
+                off2 = pk2(off, off);
+            }
+        };
+        bool ok = true;
+        for (int it = k0, i = 0; it < k1; ++it, ++i) {
+            const int pi = G::kPairs ? i >> 1 : i;
+            const int ps = pi % G::kPStages, b = i % G::kBBufs;
+            if (kByGroup ? it * BK >= next_start : true) {
+#pragma unroll
+                for (int q = 0; q < GPS; ++q) {
+                    s[q] = s_nx[q];
+                    z[q] = z_nx[q];
+                }
+                if constexpr (kByGroup) {
+                    ++cur_g;
+                    next_start = cur_g * a.g;
+                    fetch(cur_g);
+                } else {
+                    fetch(it + 1);
+                }
+                if constexpr (GPS == 1) set(0);
+            }
+            if (!mbar_wait(&bars->pfull[ps], (pi / G::kPStages) & 1u, abort) ||
+                !mbar_wait(&bars->bempty[b], ((i / G::kBBufs) & 1u) ^ 1u, abort)) {
+                ok = false;
+                break;
+            }
+            const uint8_t* src = pbuf + ps * G::kSlot;
+            if constexpr (BITS != 3) {
+                src += j * G::kRowBytes;
+            } else if constexpr (MODE == kBack) {
+                src += (j >> 7) * (BK * G::kRowBytes) + (j & 63) * G::kRowBytes + ((j >> 6) & 1) * (G::kRowBytes / 2);
+            } else {
+                src += j * G::kRowBytes + (i & 1) * (G::kRowBytes / 2);
+            }
+            uint32_t w[2 * BITS];
+            load_words<BITS>(src, w);
+            const uint32_t row = smem_u32(bbuf + b * kBBytes) + j * 128;
+#pragma unroll
+            for (int c = 0; c < BK / 8; ++c) {
+                if constexpr (GPS > 1) {
+                    if (c % (8 / GPS) == 0) set(c / (8 / GPS));
+                }
+                uint32_t o[4];
+                if constexpr (kTable) lookup<BITS>(w, c, tab, o);
+                else direct8(w, c, s2, off2, o);
+                sts128_u(row + ((c ^ (j & 7)) << 4), make_uint4(o[0], o[1], o[2], o[3]));
+            }
+            fence_async_smem();
+            mbar_arrive(&bars->bfull[b]);
+            // the slot's words have been used (their loads completed) before it may be refilled
+            if (!G::kPairs || (i & 1) || it + 1 == k1) mbar_arrive(&bars->pempty[ps]);
+        }
+        // ------------------------------------------------ drain: tensor memory -> output
+        if (ok && mbar_wait(&bars->acc_full, 0, abort)) {
+            tc_fence_after();
+            const int q = warp & 3;           // tensor-memory lane quarter of this warp
+            const int side = (warp - 2) >> 2; // it shares the quarter's chunks with one other warp
+            const int chunks = MODE == kGated && slot < 0 ? TN / 64 : TN / 32;
+#pragma unroll 1
+            for (int e = side; e < halves * chunks; e += 2) {
+                const int h = e / chunks, c = e % chunks;
+                const int t = t0 + h * 128 + 32 * q + lane;
+                const uint32_t at = tmem + (static_cast<uint32_t>(32 * q) << 16) + h * TN + c * 32;
+                float v[32], u[32];
+                tmem_ld32(at, v);
+                if constexpr (MODE == kGated) {
+                    if (slot < 0) tmem_ld32(at + TN / 2, u);
+                }
+                if (t < a.n_tok && slot >= 0) {
+                    float* p = a.part + (static_cast<int64_t>(slot) * a.part_rows + (t - t0)) * TN + c * 32;
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        reinterpret_cast<float4*>(p)[x] = make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+                } else if (t < a.n_tok) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        float vv[8], uu[8];
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) {
+                            vv[y] = v[8 * x + y];
+                            uu[y] = MODE == kGated ? u[8 * x + y] : 0.f;
+                        }
+                        emit8<MODE>(a, t, n0 + c * 32 + 8 * x, vv, uu);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+    if (threadIdx.x == 0 && bars->abort) report(a.status, GPTQ_ERR_TIMEOUT);
+}
+
+// The split tiles: their parts added in order, then the epilogue.  One thread
+// per 8 outputs of a token.
+template <int MODE>
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args a, int split_tiles) {
+    constexpr int kOut = MODE == kGated ? TN / 2 : TN;
+    const int64_t per_tile = static_cast<int64_t>(a.part_rows) * (kOut / 8);
+    const int64_t total = per_tile * split_tiles;
+    for (int64_t e = blockIdx.x * 256ll + threadIdx.x; e < total; e += gridDim.x * 256ll) {
+        const int i = static_cast<int>(e / per_tile), r = static_cast<int>(e % per_tile);
+        const int row = r / (kOut / 8), c = (r % (kOut / 8)) * 8;
+        const int tile = a.full + i;
+        const int t = (tile / a.tiles_n) * TM + row, n = (tile % a.tiles_n) * kOut + c;
+        if (t >= a.n_tok || n >= a.N) continue;
+        float v[8] = {}, u[8] = {};
+        for (int k = 0; k < a.split; ++k) {
+            const float* p = a.part + ((static_cast<int64_t>(i) * a.split + k) * a.part_rows + row) * TN + c;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const float4 q = reinterpret_cast<const float4*>(p)[x];
+                v[4 * x] += q.x; v[4 * x + 1] += q.y; v[4 * x + 2] += q.z; v[4 * x + 3] += q.w;
+                if constexpr (MODE == kGated) {
+                    const float4 w = reinterpret_cast<const float4*>(p + TN / 2)[x];
+                    u[4 * x] += w.x; u[4 * x + 1] += w.y; u[4 * x + 2] += w.z; u[4 * x + 3] += w.w;
+                }
+            }
+        }
+        emit8<MODE>(a, t, n, v, u);
+    }
+}
+
+// Tiles of the output, how many of them run whole, and into how many parts of
+// `per` stages each of the others is split.
+struct Plan {
+    int tiles_n, tiles_t, full, split, per, part_rows;
+    size_t part_bytes;
+};
+
+Plan make_plan(int64_t n_tok, int64_t N, int nk, bool gated, bool pairs) {
+    Plan p;
+    const int out = gated ? TN / 2 : TN;
+    p.tiles_n = static_cast<int>((N + out - 1) / out);
+    p.tiles_t = static_cast<int>((n_tok + TM - 1) / TM);
+    const int64_t tiles = static_cast<int64_t>(p.tiles_n) * p.tiles_t;
+    p.full = static_cast<int>(tiles);
+    p.split = 1;
+    p.per = nk;
+    p.part_rows = static_cast<int>(n_tok < TM ? n_tok : TM);
+    p.part_bytes = 0;
+    const int rest = static_cast<int>(tiles % kSms);
+    int split = rest > 0 ? kSms / rest : 1;
+    if (split > kMaxSplit) split = kMaxSplit;
+    if (split > nk / kMinStages) split = nk / kMinStages;
+    if (split > 1) {
+        int per = (nk + split - 1) / split;
+        if (pairs) per = (per + 1) / 2 * 2;   // a packed slot serves two stages
+        split = (nk + per - 1) / per;
+        if (split > 1) {
+            p.full = static_cast<int>(tiles) - rest;
+            p.split = split;
+            p.per = per;
+            p.part_bytes = static_cast<size_t>(rest) * split * p.part_rows * TN * sizeof(float);
+        }
+    }
+    return p;
+}
+
+template <int BITS, int GPS, int MODE>
+cudaError_t launch_one(const CUtensorMap (&ta)[2], const CUtensorMap (&tp)[2], const Args& a, int units,
+                       cudaStream_t stream) {
+    auto kern = packed_gemm_kernel<BITS, GPS, MODE>;
+    constexpr int kSmem = Geom<BITS, MODE>::kSmem;
+    static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    kern<<<units, kThreads, kSmem, stream>>>(ta[0], ta[1], tp[0], tp[1], a);
+    return cudaGetLastError();
+}
+
+template <int BITS, int MODE>
+cudaError_t launch_groups(const CUtensorMap (&ta)[2], const CUtensorMap (&tp)[2], const Args& a, int units,
+                          cudaStream_t stream) {
+    const int g = a.g;
+    if (g % 64 == 0 || g >= a.d_col) return launch_one<BITS, 1, MODE>(ta, tp, a, units, stream);
+    if (g == 32) return launch_one<BITS, 2, MODE>(ta, tp, a, units, stream);
+    if (g == 16) return launch_one<BITS, 4, MODE>(ta, tp, a, units, stream);
+    return launch_one<BITS, 8, MODE>(ta, tp, a, units, stream);
+}
+
+template <int MODE>
+gptq_status run(Args a, const CUtensorMap (&ta)[2], const uint32_t* const (&packed)[2], int bits, bool pairs,
+                void* part, int64_t* launches, cudaStream_t stream) {
+    const Plan p = make_plan(a.n_tok, a.N, a.nk, MODE == kGated, pairs);
+    a.tiles_n = p.tiles_n; a.tiles_t = p.tiles_t;
+    a.full = p.full; a.split = p.split; a.per = p.per; a.part_rows = p.part_rows;
+    a.part = static_cast<float*>(part);
+    const int rest = p.tiles_n * p.tiles_t - p.full;
+    const int units = p.full + rest * p.split;
+    // the packed words move as raw 32-bit elements (the map's fp32 type only sizes them)
+    const uint64_t words = static_cast<uint64_t>(a.d_col) * bits / 32;
+    const uint32_t box = static_cast<uint32_t>((bits == 3 ? 128 : 64) * bits / 32);
+    CUtensorMap tp[2];
+    for (int m = 0; m < 2; ++m)
+        if (!make_tmap_2d(&tp[m], false, packed[m], words, a.d_row, words, box, MODE == kBack ? BK : 128, Swz::kNone))
+            return GPTQ_ERR_INVALID_ARG;
+    cudaError_t e;
+    switch (bits) {
+        case 2: e = launch_groups<2, MODE>(ta, tp, a, units, stream); break;
+        case 3: e = launch_groups<3, MODE>(ta, tp, a, units, stream); break;
+        case 4: e = launch_groups<4, MODE>(ta, tp, a, units, stream); break;
+        default: e = launch_groups<8, MODE>(ta, tp, a, units, stream); break;
+    }
+    if (e != cudaSuccess) return GPTQ_ERR_CUDA;
+    ++*launches;
+    if (rest > 0) {
+        const int64_t work = static_cast<int64_t>(rest) * a.part_rows * ((MODE == kGated ? TN / 2 : TN) / 8);
+        const int64_t want = (work + 255) / 256;
+        join_kernel<MODE><<<static_cast<int>(want < 16 * kSms ? want : 16 * kSms), 256, 0, stream>>>(a, rest);
+        if (cudaGetLastError() != cudaSuccess) return GPTQ_ERR_CUDA;
+        ++*launches;
+    }
+    return GPTQ_OK;
+}
+
+size_t round256(size_t b) { return (b + 255) / 256 * 256; }
+
+}  // namespace
+
+size_t linear_gemm_workspace_bytes(int64_t n_tok, int64_t d_col, int64_t d_row, bool gated) {
+    const Plan p = make_plan(n_tok, d_row, static_cast<int>(d_col / BK), gated, true);
+    const Plan q = make_plan(n_tok, d_row, static_cast<int>(d_col / BK), gated, false);
+    return round256(static_cast<size_t>(n_tok) * d_col * 2) +
+           round256(p.part_bytes > q.part_bytes ? p.part_bytes : q.part_bytes);
+}
+
+gptq_status launch_linear_gemm(const LinearCall& c, cudaStream_t stream) {
+    const bool gated = c.mat[1].packed != nullptr;
+    int64_t launches = 0;
+    const uint16_t* A = c.X;
+    int64_t lda = c.ldx;
+    if (needs_gather(c.X, c.ldx, c.perm)) {
+        uint16_t* xq = static_cast<uint16_t*>(c.ws);
+        if (launch_gather_bf16(c.X, c.ldx, c.n_tok, static_cast<int>(c.d_col), c.perm, xq, stream) != cudaSuccess)
+            return GPTQ_ERR_CUDA;
+        A = xq;
+        lda = c.d_col;
+        ++launches;
+    }
+    CUtensorMap ta[2];
+    if (!make_tmap_2d(&ta[0], true, A, c.d_col, c.n_tok, lda, BK, 128, Swz::k128)) return GPTQ_ERR_INVALID_ARG;
+    ta[1] = ta[0];
+    Args a = {};
+    a.mat[0] = c.mat[0];
+    a.mat[1] = c.mat[1];
+    a.n_tok = static_cast<int>(c.n_tok);
+    a.N = static_cast<int>(c.d_row);
+    a.d_row = static_cast<int>(c.d_row);
+    a.d_col = static_cast<int>(c.d_col);
+    a.nk = a.nk1 = a.d_col / BK;
+    a.g = (c.group == -1 || c.group > a.d_col) ? a.d_col : c.group;
+    a.bias = c.bias;
+    a.act = c.act;
+    a.residual = c.residual; a.ldr = c.ldr;
+    for (int m = 0; m < 2; ++m) {
+        a.pre[m] = c.pre[m];
+        a.ldpre[m] = c.ldpre[m];
+    }
+    a.Y = c.Y; a.ldy = c.ldy;
+    a.status = c.status;
+    void* part = static_cast<uint8_t*>(c.ws) + round256(static_cast<size_t>(c.n_tok) * c.d_col * 2);
+    const uint32_t* packed[2] = {c.mat[0].packed, gated ? c.mat[1].packed : c.mat[0].packed};
+    const gptq_status s = gated ? run<kGated>(a, ta, packed, c.bits, c.bits == 3, part, &launches, stream)
+                                : run<kLinear>(a, ta, packed, c.bits, c.bits == 3, part, &launches, stream);
+    count_launches(launches);
+    return s;
+}
+
+// Whether the call reads its workspace at all.
+bool linear_gemm_needs_workspace(const LinearCall& c) {
+    const Plan p = make_plan(c.n_tok, c.d_row, static_cast<int>(c.d_col / BK), c.mat[1].packed != nullptr, c.bits == 3);
+    return p.part_bytes > 0 || needs_gather(c.X, c.ldx, c.perm);
+}
+
+// ---- gradients: the slopes (linear_backward.cu), then dXq = dP W here, then
+// the columns back in the input's order.  Workspace: dXq (with a permutation),
+// the partial tiles, the partial bias gradients.
+namespace {
+int back_stages(int64_t d_row, bool gated) { return static_cast<int>((d_row + BK - 1) / BK) * (gated ? 2 : 1); }
+}  // namespace
+
+size_t linear_backward_workspace_bytes(int64_t n_tok, int64_t d_col, int64_t d_row, bool gated) {
+    const Plan p = make_plan(n_tok, d_col, back_stages(d_row, gated), false, false);
+    return round256(static_cast<size_t>(n_tok) * d_col * 2) + round256(p.part_bytes) +
+           (gated ? 0 : round256(bias_partial_bytes(n_tok, d_row)));
+}
+
+gptq_status launch_linear_backward(const BackwardCall& c, cudaStream_t stream) {
+    const bool gated = c.mat[1].packed != nullptr;
+    int64_t launches = 0;
+    uint8_t* ws = static_cast<uint8_t*>(c.ws);
+    const size_t at_part = round256(static_cast<size_t>(c.n_tok) * c.d_col * 2);
+    const Plan p = make_plan(c.n_tok, c.d_col, back_stages(c.d_row, gated), false, false);
+    float* bias_part = c.dbias == nullptr ? nullptr : reinterpret_cast<float*>(ws + at_part + round256(p.part_bytes));
+    gptq_status s = launch_slopes(c, bias_part, &launches, stream);
+    if (s != GPTQ_OK) return s;
+    CUtensorMap ta[2];
+    for (int m = 0; m < 2; ++m) {
+        // the gradient of the products: dPre / dGate, dUp, or dY itself
+        const int k = gated ? m : 0;
+        const uint16_t* D = c.dP[k] != nullptr ? c.dP[k] : c.dY;
+        const int64_t ld = c.dP[k] != nullptr ? c.lddp[k] : c.lddy;
+        if (!make_tmap_2d(&ta[m], true, D, c.d_row, c.n_tok, ld, BK, 128, Swz::k128)) return GPTQ_ERR_INVALID_ARG;
+    }
+    Args a = {};
+    a.mat[0] = c.mat[0];
+    a.mat[1] = gated ? c.mat[1] : c.mat[0];
+    a.n_tok = static_cast<int>(c.n_tok);
+    a.N = a.d_col = static_cast<int>(c.d_col);
+    a.d_row = static_cast<int>(c.d_row);
+    a.nk = back_stages(c.d_row, gated);
+    a.nk1 = back_stages(c.d_row, false);
+    a.g = (c.group == -1 || c.group > a.d_col) ? a.d_col : c.group;
+    a.Y = c.perm != nullptr ? reinterpret_cast<uint16_t*>(ws) : c.dX;
+    a.ldy = c.perm != nullptr ? c.d_col : c.lddx;
+    a.status = c.status;
+    const uint32_t* packed[2] = {a.mat[0].packed, a.mat[1].packed};
+    s = run<kBack>(a, ta, packed, c.bits, false, ws + at_part, &launches, stream);
+    if (s == GPTQ_OK && c.perm != nullptr) {
+        s = launch_scatter(reinterpret_cast<const uint16_t*>(ws), c.n_tok, static_cast<int>(c.d_col), c.perm, c.dX,
+                           c.lddx, stream);
+        ++launches;
+    }
+    count_launches(launches);
+    return s;
+}
+
+// Whether the call reads its workspace at all.
+bool linear_backward_needs_workspace(const BackwardCall& c) {
+    const bool gated = c.mat[1].packed != nullptr;
+    const Plan p = make_plan(c.n_tok, c.d_col, back_stages(c.d_row, gated), false, false);
+    return c.perm != nullptr || p.part_bytes > 0 || c.dbias != nullptr;
+}
+
+}  // namespace gptq

@@ -57,8 +57,7 @@ class Layer:
 
 
 def rng_of(*key):
-    return np.random.default_rng(abs(hash(tuple(key))) % (1 << 32) if any(isinstance(k, str) for k in key)
-                                 else sum((i + 1) * 7919 * int(k) for i, k in enumerate(key)) + 11)
+    return np.random.default_rng(sum((i + 1) * 7919 * int(k) for i, k in enumerate(key)) + 11)
 
 
 def bf16(rng, *shape, std=1.0):
@@ -91,10 +90,12 @@ def act(x, name):
     return 0.5 * x * (1 + t), 0.5 * (1 + t) + 0.5 * x * (1 - t * t) * c * (1 + 3 * 0.044715 * x * x)
 
 
-# Largest slope of any of the activations (GELU: 1 + 0.129), and of their
-# slopes' error against fp32 evaluation: 16 fp32 roundings of values <= 2.
+# Largest slope of any of the activations (GELU: 1 + 0.129).
 LIPSCHITZ = 1.13
-ACT_EPS = 16 * EPS32
+# Relative error of an activation and absolute error of a slope (at most 1.13)
+# in fp32: exp's argument y carries a rounding of |y| 2^-24, |y| < 104 where
+# the result has not underflowed, so 52 units of 2^-23, and a dozen roundings.
+ACT_EPS = 64 * EPS32
 
 
 def ordered(X, perm):
@@ -160,3 +161,72 @@ def check(got, want, bound, what):
     worst = np.max(err / bound)
     print(f"{what}: max |err| / bound {worst:.3f}")
     assert worst <= 1.0, f"{what}: {worst} at {np.unravel_index(np.argmax(err / bound), err.shape)}"
+
+
+def slopes_linear(dY, pre, activation):
+    """(dP, bound) in float64."""
+    d = f64(dY)
+    if activation == "none":
+        return d, HALF_BF16 * np.abs(d)
+    p = d * act(f64(pre), activation)[1]
+    return p, rounded_bound(p, np.abs(d) * ACT_EPS)
+
+
+def slopes_gated(dY, gate, up, activation):
+    """((dG, bound), (dU, bound)) in float64."""
+    d, u = f64(dY), f64(up)
+    v, sl = act(f64(gate), activation)
+    dg, du = d * u * sl, d * v
+    return ((dg, rounded_bound(dg, np.abs(d * u) * ACT_EPS)),
+            (du, rounded_bound(du, np.abs(du) * ACT_EPS + 1e-30)))
+
+
+def back_product(dPs, layers, perm):
+    """(dX, bound) in float64 from the bf16 gradients that the call wrote: at
+    most one rounding per 16 terms plus the sums inside a step, each within
+    2^-23 of the sum of magnitudes (twice that allowed), plus the joins."""
+    y = e = 0
+    for d, layer in zip(dPs, layers):
+        w = layer.weights(True)
+        y = y + f64(d) @ w
+        e = e + np.abs(f64(d)) @ np.abs(w)
+    terms = sum(d.shape[1] for d in dPs)
+    bound = rounded_bound(y, 2 * (terms / 16 + 64) * EPS32 * e)
+    if perm is not None:
+        out, ob = np.empty_like(y), np.empty_like(y)
+        out[:, perm], ob[:, perm] = y, bound
+        return out, ob
+    return y, bound
+
+
+def padded(t, ld, fill=float("nan"), offset=0):
+    """t's values as a view of a wider CUDA buffer whose other entries are `fill`."""
+    n, c = t.shape
+    buf = torch.full((n * ld + offset,), fill, dtype=t.dtype, device="cuda")
+    v = buf[offset:offset + n * ld].view(n, ld)[:, :c]
+    v.copy_(t)
+    return buf, v
+
+
+def blank(n, c, ld=None):
+    """An n x c bf16 output of NaNs in a buffer whose other entries are 7."""
+    ld = c + 3 if ld is None else ld
+    buf = torch.full((n, ld), 7.0, dtype=torch.bfloat16, device="cuda")
+    v = buf[:, :c]
+    v.fill_(float("nan"))
+    return buf, v
+
+
+def untouched(buf, c):
+    assert torch.all(buf[:, c:] == 7.0), "written outside the output"
+
+
+def cuda(x):
+    if x is None:
+        return None
+    return x.cuda() if isinstance(x, torch.Tensor) else torch.from_numpy(x).cuda()
+
+
+def workspace(size):
+    """A workspace of exactly `size` bytes full of NaN bit patterns."""
+    return torch.full((size,), 255, dtype=torch.uint8, device="cuda") if size else None

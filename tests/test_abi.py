@@ -302,6 +302,133 @@ def test_dequant_gemm_validation(pkg):
     assert call(ws=ctypes.c_void_p((1 << 20) + 32)) == 6
 
 
+# The products with an epilogue: everything below is answered on the host.
+_P, _I64, _I32, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
+_A, _B = ctypes.c_void_p(1 << 20), ctypes.c_void_p(1 << 24)
+
+
+def _odd(by):
+    return ctypes.c_void_p((1 << 20) + by)
+
+
+_LAYER = ("pk", "sc", "ze")
+_LAYERS = ("pk", "sc", "ze", "pk2", "sc2", "ze2")
+_EPILOGUE = {
+    # name: argument order (argument: type by its name in _TYPES)
+    "gptq_dequant_matmul_linear": ("X", "n", "k", "ldx", *_LAYER, "perm", "r", "bits", "g", "bias", "act", "res",
+                                   "ldr", "Y", "ldy", "ws", "wsb", "stream"),
+    "gptq_dequant_matmul_gated": ("X", "n", "k", "ldx", *_LAYERS, "perm", "r", "bits", "g", "act", "Y", "ldy", "ws",
+                                  "wsb", "stream"),
+    "gptq_dequant_gemm_linear": ("X", "n", "k", "ldx", *_LAYER, "perm", "r", "bits", "g", "bias", "act", "res", "ldr",
+                                 "pre", "ldpre", "Y", "ldy", "st", "ws", "wsb", "stream"),
+    "gptq_dequant_gemm_gated": ("X", "n", "k", "ldx", *_LAYERS, "perm", "r", "bits", "g", "act", "gate", "ldgate",
+                                "up", "ldup", "Y", "ldy", "st", "ws", "wsb", "stream"),
+    "gptq_dequant_gemm_linear_backward": ("dY", "n", "r", "lddy", *_LAYER, "perm", "k", "bits", "g", "act", "pre",
+                                          "ldpre", "dPre", "lddpre", "dbias", "dX", "lddx", "st", "ws", "wsb",
+                                          "stream"),
+    "gptq_dequant_gemm_gated_backward": ("dY", "n", "r", "lddy", "gate", "ldgate", "up", "ldup", *_LAYERS, "perm",
+                                         "k", "bits", "g", "act", "dGate", "lddgate", "dUp", "lddup", "dX", "lddx",
+                                         "st", "ws", "wsb", "stream"),
+}
+_SIZES = {"gptq_dequant_matmul_linear": 2, "gptq_dequant_matmul_gated": 2, "gptq_dequant_gemm_linear": 3,
+          "gptq_dequant_gemm_gated": 3, "gptq_dequant_gemm_linear_backward": 3,
+          "gptq_dequant_gemm_gated_backward": 3}
+
+
+def _epilogue(pkg, name):
+    lib = ctypes.CDLL(pkg.library_path())
+    order = _EPILOGUE[name]
+
+    def kind(a):
+        if a in ("bits", "g", "act"):
+            return _I32
+        return _SZ if a == "wsb" else _I64 if a in ("n", "k", "r") or a.startswith("ld") else _P
+
+    f = _entry(lib, name, [kind(a) for a in order])
+    size = _entry(lib, name + "_workspace_size", [_I64] * _SIZES[name], _SZ)
+    need = size(*(16, 256, 136)[:_SIZES[name]])
+    ok = {a: _A if kind(a) is _P else None for a in order}
+    ok.update(n=16, k=256, r=136, bits=4, g=128, act=0, wsb=need, st=None, stream=None, dX=_B, Y=_B, dUp=_B)
+    ok.update({a: 256 if a in ("ldx", "lddx") else 136 for a in order if a.startswith("ld")})
+    ok = {a: ok[a] for a in order}
+    return _caller(f, order, ok), order, size, need
+
+
+@pytest.mark.parametrize("name", sorted(_EPILOGUE))
+def test_products_with_an_epilogue_refuse_on_the_host(pkg, name):
+    call, order, size, need = _epilogue(pkg, name)
+    if "matmul" in name:
+        assert size(16, 256) == 16 * 256 * 2 and size(100, 256) == 32 * 256 * 2   # 32 tokens per launch
+        assert size(0, 256) == 0 and size(1, 0) == 0
+    else:
+        assert need >= 16 * 256 * 2 and need % 256 == 0
+        assert size(0, 256, 136) == 0 and size(1, 0, 136) == 0 and size(1, 256, 0) == 0
+        assert size((1 << 24) + 1, 256, 136) == 0
+    needed = [a for a in order if a in ("X", "Y", "dY", "dX", "pk", "sc", "ze", "pk2", "sc2", "ze2", "dGate", "dUp")]
+    if "backward" in name:
+        needed += [a for a in ("gate", "up") if a in order]
+    for a in needed:
+        assert call(**{a: None}) == 1, a
+    for a in order:
+        if a.startswith("ld") and a != "lddpre":
+            kw = {a: 135 if a not in ("ldx", "lddx") else 255}
+            if a == "ldpre" and "backward" in name:
+                kw["act"] = 2
+            assert call(**kw) == 1, a
+    assert call(n=-1) == 1 and call(n=(1 << 24) + 1) == 1 and call(k=0) == 1 and call(r=0) == 1
+    for bits in (0, 1, 5, 16):
+        assert call(bits=bits) == 1
+    assert call(g=0) == 1 and call(g=-2) == 1 and call(act=-1) == 1 and call(act=5) == 1
+    for a in ("pk", "pk2"):
+        if a in order:
+            assert call(**{a: _odd(8)}) == 1               # packed rows by 16-byte units
+    for a in ("sc", "ze", "sc2", "ze2", "perm", "bias", "dbias"):
+        if a in order:
+            assert call(**{a: _odd(2)}) == 1, a
+    for a in ("X", "Y", "res", "dX", "gate", "up", "dGate", "dUp", "dPre"):
+        if a in order:
+            assert call(**{a: _odd(1)}) == 1, a
+    # shapes the kernels do not take
+    wide = {a: 1 << 25 for a in order if a.startswith("ld")}
+    assert call(k=224, **wide) == 2 and call(k=192, bits=3, **wide) == 2
+    assert call(k=(1 << 24) + 64, **wide) == 2 and call(r=(1 << 24) + 8, **wide) == 2
+    for g in (1, 4, 12, 24, 48, 96, 200):
+        assert call(g=g) == 2, g
+    # a permutation needs the workspace
+    assert call(ws=None) == 6 and call(wsb=need - 1) == 6
+    assert call(ws=ctypes.c_void_p((1 << 20) + 128)) == 6
+    if "dbias" not in order:
+        assert call(n=0) == 0
+
+
+def test_gradients_need_rows_of_whole_16_byte_units(pkg):
+    call, _, _, _ = _epilogue(pkg, "gptq_dequant_gemm_linear_backward")
+    assert call(dPre=_odd(8)) == 1 and call(lddpre=140) == 1 and call(lddpre=128) == 1
+    # dY itself is read by the tensor memory accelerator where there is no dPre
+    assert call(dPre=None, dY=_odd(2)) == 1 and call(dPre=None, lddy=140) == 1
+    assert call(dPre=None, act=4) == 1                     # an activation needs dPre
+    assert call(act=4, pre=None) == 1                      # and the saved sums
+    call, _, _, _ = _epilogue(pkg, "gptq_dequant_gemm_gated_backward")
+    assert call(dUp=_odd(8)) == 1 and call(lddup=140) == 1 and call(dGate=_odd(8)) == 1
+    assert call(dUp=_A) == 1                               # dGate and dUp are apart
+
+
+def test_python_products_with_an_epilogue_refuse_on_the_cpu(pkg):
+    """Tensors that are not on a CUDA device never reach the library."""
+    import torch
+    x = torch.zeros(2, 64, dtype=torch.bfloat16)
+    layer = (torch.zeros(8, 8, dtype=torch.int32), torch.zeros(1, 8), torch.zeros(1, 8, dtype=torch.int32))
+    y = torch.zeros(2, 8, dtype=torch.bfloat16)
+    for call in (lambda: pkg.gptq_dequant_matmul_linear(x, *layer, None, 4, 64, y),
+                 lambda: pkg.gptq_dequant_matmul_gated(x, *layer, *layer, None, 4, 64, "silu", y),
+                 lambda: pkg.gptq_dequant_gemm_linear(x, *layer, None, 4, 64, y),
+                 lambda: pkg.gptq_dequant_gemm_gated(x, *layer, *layer, None, 4, 64, "silu", y),
+                 lambda: pkg.gptq_dequant_gemm_linear_backward(y, *layer, None, 4, 64, x),
+                 lambda: pkg.gptq_dequant_gemm_gated_backward(y, y, y, *layer, *layer, None, 4, 64, "silu", y, y, x)):
+        with pytest.raises(TypeError):
+            call()
+
+
 C_CLIENT = r"""
 #include <stdio.h>
 #include <string.h>
