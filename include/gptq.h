@@ -408,7 +408,11 @@ typedef enum gptq_activation {
 /*
  * Decode form, for a few tokens: tokens are taken up to 32 per launch and each
  * launch reads the packed layer once.  W[n][k] = scales[k/g][n] * (code[n][k] -
- * zeros[k/g][n]) enters unrounded, as in gptq_dequant_matmul.
+ * zeros[k/g][n]) enters unrounded, as in gptq_dequant_matmul.  Activations of
+ * magnitude 2^63 and more count as infinite; those below 2^-57 contribute with
+ * an absolute error of up to 2^-80 times the weight.
+ *   dev_status  device int32 (may be NULL) receiving GPTQ_ERR_TIMEOUT if a
+ *       bounded wait runs out.
  *   ws  gptq_dequant_matmul_linear_workspace_size(n_tok, d_col) bytes, used when
  *       perm is given or X's rows are not 16-byte aligned; may be NULL otherwise.
  */
@@ -417,15 +421,16 @@ gptq_status gptq_dequant_matmul_linear(const uint16_t *X, int64_t n_tok, int64_t
                                        const int32_t *zeros, const int32_t *perm, int64_t d_row,
                                        int32_t bits, int32_t group_size, const float *bias,
                                        int32_t activation, const uint16_t *residual, int64_t ldr,
-                                       uint16_t *Y, int64_t ldy, void *ws, size_t ws_bytes,
-                                       cudaStream_t stream);
+                                       uint16_t *Y, int64_t ldy, int32_t *dev_status, void *ws,
+                                       size_t ws_bytes, cudaStream_t stream);
 gptq_status gptq_dequant_matmul_gated(const uint16_t *X, int64_t n_tok, int64_t d_col, int64_t ldx,
                                       const uint32_t *packed_gate, const float *scales_gate,
                                       const int32_t *zeros_gate, const uint32_t *packed_up,
                                       const float *scales_up, const int32_t *zeros_up,
                                       const int32_t *perm, int64_t d_row, int32_t bits,
                                       int32_t group_size, int32_t activation, uint16_t *Y,
-                                      int64_t ldy, void *ws, size_t ws_bytes, cudaStream_t stream);
+                                      int64_t ldy, int32_t *dev_status, void *ws, size_t ws_bytes,
+                                      cudaStream_t stream);
 
 /* Workspace bytes of the two (up to 32 tokens x d_col bf16); 0 for invalid sizes. */
 size_t gptq_dequant_matmul_linear_workspace_size(int64_t n_tok, int64_t d_col);

@@ -108,10 +108,10 @@ def _load():
                                ctypes.c_size_t, P], ctypes.c_int),
         "gptq_dequant_gemm_workspace_size": ([i64, i64], ctypes.c_size_t),
         "gptq_dequant_matmul_linear": ([P, i64, i64, i64, P, P, P, P, i64, i32, i32, P, i32, P, i64,
-                                        P, i64, P, ctypes.c_size_t, P], ctypes.c_int),
+                                        P, i64, P, P, ctypes.c_size_t, P], ctypes.c_int),
         "gptq_dequant_matmul_linear_workspace_size": ([i64, i64], ctypes.c_size_t),
         "gptq_dequant_matmul_gated": ([P, i64, i64, i64, P, P, P, P, P, P, P, i64, i32, i32, i32,
-                                       P, i64, P, ctypes.c_size_t, P], ctypes.c_int),
+                                       P, i64, P, P, ctypes.c_size_t, P], ctypes.c_int),
         "gptq_dequant_matmul_gated_workspace_size": ([i64, i64], ctypes.c_size_t),
         "gptq_dequant_gemm_linear": ([P, i64, i64, i64, P, P, P, P, i64, i32, i32, P, i32, P, i64,
                                       P, i64, P, i64, P, P, ctypes.c_size_t, P], ctypes.c_int),
@@ -438,100 +438,132 @@ def _activation(name) -> int:
     return ACTIVATIONS[name]
 
 
-def _bytes(ws: torch.Tensor | None) -> int:
-    return 0 if ws is None else ws.numel() * ws.element_size()
+# The products with an epilogue check their operands through the helpers below:
+# few attribute reads per tensor (a decode step's kernel runs a few
+# microseconds, and the checks are on its critical path).
+_Tensor = torch.Tensor
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _packed_layer(X: torch.Tensor, x_name: str, packed, scales, zeros, bits: int, group_size: int,
-                  d_col: int, suffix: str = "") -> int:
-    """Checks the shapes of one packed layer whose input width is d_col, and
-    returns its d_row."""
-    _cuda(packed, "packed" + suffix, torch.int32)
-    _cuda(scales, "scales" + suffix, torch.float32)
-    _cuda(zeros, "zeros" + suffix, torch.int32)
-    _same_device(X, x_name, (packed, "packed" + suffix, None), (scales, "scales" + suffix, None),
-                 (zeros, "zeros" + suffix, None))
-    for t, name in ((packed, "packed"), (scales, "scales"), (zeros, "zeros")):
-        if not t.is_contiguous():
-            raise ValueError(f"{name}{suffix} must be contiguous")
-    if int(group_size) < 1 and int(group_size) != -1:
-        return packed.shape[0]   # the library's own refusal follows
-    d_row = packed.shape[0]
-    ng = n_groups(d_col, int(group_size))
-    if tuple(packed.shape) != (d_row, packed_words(d_col, int(bits))):
-        raise ValueError(f"packed{suffix} must be d_row x {packed_words(d_col, int(bits))} words, "
-                         f"got {tuple(packed.shape)}")
-    for t, name in ((scales, "scales"), (zeros, "zeros")):
-        if tuple(t.shape) != (ng, d_row):
-            raise ValueError(f"{name}{suffix} must be {ng} x {d_row}, got {tuple(t.shape)}")
-    return d_row
+def _refuse(t, name: str, dtype, dev: int) -> None:
+    """Raises for an operand that is not a `dtype` tensor on cuda:dev."""
+    if not isinstance(t, _Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    raise ValueError(f"{name} must be on cuda:{dev} like the first operand, not on {t.device}")
 
 
-def _rows(ref: torch.Tensor, ref_name: str, t: torch.Tensor | None, name: str, n: int,
-          cols: int) -> int:
-    """An n x cols bf16 matrix with contiguous rows on ref's device (None
-    passes); returns its leading dimension."""
+def _first(t, name: str) -> int:
+    """The device index of a call's first operand (bf16), which has to be the
+    current device: the library launches there."""
+    if not isinstance(t, _Tensor) or t.dtype is not _BF16 or not t.is_cuda:
+        _refuse(t, name, _BF16, 0)
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on cuda:{dev} but cuda:{torch.cuda.current_device()} is current: "
+                         "make its device current (torch.cuda.device(...))")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D with contiguous rows")
+    return dev
+
+
+def _launch_stream(stream, dev: int):
+    if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(dev)
+        stream = torch.cuda.current_stream()
+    return getattr(stream, "cuda_stream", stream)
+
+
+def _pitch(t: torch.Tensor, name: str) -> int:
+    """Leading dimension of a 2-D tensor with contiguous, separate rows."""
+    n, c = t.shape
+    ld, step = t.stride()
+    if (step != 1 and c > 1) or (n > 1 and ld < c):
+        raise ValueError(f"{name} must have contiguous rows that do not overlap (strides {t.stride()})")
+    return ld if ld > c else c
+
+
+def _rows(t, name: str, n: int, cols: int, dev: int) -> int:
+    """Leading dimension of an n x cols bf16 operand (0 for None)."""
     if t is None:
         return 0
-    _cuda(t, name, torch.bfloat16)
-    _same_device(ref, ref_name, (t, name, None))
-    if tuple(t.shape) != (n, cols):
+    if not isinstance(t, _Tensor) or t.dtype is not _BF16 or t.get_device() != dev:
+        _refuse(t, name, _BF16, dev)
+    if t.shape != (n, cols):
         raise ValueError(f"{name} must be {n} x {cols}, got {tuple(t.shape)}")
-    return _leading(t, name)
+    return _pitch(t, name)
 
 
-def _leading(t: torch.Tensor, name: str) -> int:
-    """_row_major for an operand that may be written or be one row of a wider
-    buffer: a stride below the row length (an expanded tensor) is refused."""
-    ld = _row_major(t, name)
-    if t.shape[0] > 1 and ld < t.shape[1]:
-        raise ValueError(f"the rows of {name} overlap (strides {t.stride()})")
-    return ld
-
-
-def _vector(ref: torch.Tensor, ref_name: str, t: torch.Tensor | None, name: str, n: int) -> None:
+def _whole(t, name: str, dtype, shape: tuple, dev: int):
+    """Address of a contiguous operand of this shape (None for None)."""
     if t is None:
-        return
-    _cuda(t, name, torch.float32)
-    _same_device(ref, ref_name, (t, name, None))
-    if tuple(t.shape) != (n,) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous vector of {n}")
+        return None
+    if not isinstance(t, _Tensor) or t.dtype is not dtype or t.get_device() != dev:
+        _refuse(t, name, dtype, dev)
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, {' x '.join(map(str, shape))}; got {tuple(t.shape)}")
+    return t.data_ptr()
 
 
-def _order(ref: torch.Tensor, ref_name: str, perm: torch.Tensor | None, d_col: int) -> None:
-    if perm is None:
-        return
-    _cuda(perm, "perm", torch.int32)
-    _same_device(ref, ref_name, (perm, "perm", None))
-    if tuple(perm.shape) != (d_col,) or not perm.is_contiguous():
-        raise ValueError(f"perm must be a contiguous vector of {d_col}")
+def _buffer(t, name: str, dev: int):
+    """(address, bytes) of a workspace."""
+    if t is None:
+        return None, 0
+    if not isinstance(t, _Tensor) or t.get_device() != dev:
+        _refuse(t, name, None, dev)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _status(t, dev: int):
+    if t is None:
+        return None
+    if not isinstance(t, _Tensor) or t.dtype is not _I32 or t.get_device() != dev:
+        _refuse(t, "dev_status", _I32, dev)
+    return t.data_ptr()
+
+
+def _layer(packed, scales, zeros, bits: int, group_size: int, d_col: int, dev: int, suffix: str = ""):
+    """Addresses of a packed layer of input width d_col, and its d_row."""
+    if not isinstance(packed, _Tensor) or packed.dtype is not _I32 or packed.get_device() != dev:
+        _refuse(packed, "packed" + suffix, _I32, dev)
+    d_row = packed.shape[0]
+    p = _whole(packed, "packed" + suffix, _I32, (d_row, -(-(d_col * bits) // 32)), dev)
+    if group_size < 1 and group_size != -1:
+        return p, _ptr(scales), _ptr(zeros), d_row   # the library refuses the group size
+    g = d_col if group_size == -1 or group_size > d_col else group_size
+    shape = (-(-d_col // g), d_row)
+    return (p, _whole(scales, "scales" + suffix, _F32, shape, dev),
+            _whole(zeros, "zeros" + suffix, _I32, shape, dev), d_row)
 
 
 def gptq_dequant_matmul_linear(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor,
                                zeros: torch.Tensor, perm: torch.Tensor | None, bits: int,
                                group_size: int, Y: torch.Tensor, ws: torch.Tensor | None = None,
                                bias: torch.Tensor | None = None, activation: str = "none",
-                               residual: torch.Tensor | None = None, stream=None) -> None:
+                               residual: torch.Tensor | None = None,
+                               dev_status: torch.Tensor | None = None, stream=None) -> None:
     """Y = act(X W_hat^T + bias) + residual for a few tokens (decode form): X
     (tokens x d_col bf16, original column order), packed / scales / zeros /
     perm as the quantizer wrote them, bias fp32, residual and Y tokens x d_row
     bf16 (residual may be Y itself); ws (bytes of
     gptq_dequant_matmul_linear_workspace_size) is needed with a permutation
     or when X's rows are not 16-byte aligned."""
-    _cuda(X, "X", torch.bfloat16)
-    ldx = _leading(X, "X")
+    dev = _first(X, "X")
     n_tok, d_col = X.shape
-    d_row = _packed_layer(X, "X", packed, scales, zeros, bits, group_size, d_col)
-    _order(X, "X", perm, d_col)
-    _vector(X, "X", bias, "bias", d_row)
-    ldr = _rows(X, "X", residual, "residual", n_tok, d_row)
-    ldy = _rows(X, "X", Y, "Y", n_tok, d_row)
-    _same_device(X, "X", (ws, "ws", None))
-    _check(_lib.gptq_dequant_matmul_linear(_ptr(X), n_tok, d_col, ldx, _ptr(packed), _ptr(scales),
-                                           _ptr(zeros), _ptr(perm), d_row, int(bits),
-                                           int(group_size), _ptr(bias), _activation(activation),
-                                           _ptr(residual), ldr, _ptr(Y), ldy, _ptr(ws), _bytes(ws),
-                                           _stream(stream)), "gptq_dequant_matmul_linear")
+    bits, group_size = int(bits), int(group_size)
+    p, s, z, d_row = _layer(packed, scales, zeros, bits, group_size, d_col, dev)
+    wsp, wsb = _buffer(ws, "ws", dev)
+    _check(_lib.gptq_dequant_matmul_linear(
+        X.data_ptr(), n_tok, d_col, _pitch(X, "X"), p, s, z, _whole(perm, "perm", _I32, (d_col,), dev),
+        d_row, bits, group_size, _whole(bias, "bias", _F32, (d_row,), dev), _activation(activation),
+        _ptr(residual), _rows(residual, "residual", n_tok, d_row, dev), _ptr(Y),
+        _rows(Y, "Y", n_tok, d_row, dev), _status(dev_status, dev), wsp, wsb,
+        _launch_stream(stream, dev)), "gptq_dequant_matmul_linear")
 
 
 def gptq_dequant_matmul_linear_workspace_size(n_tok: int, d_col: int) -> int:
@@ -543,25 +575,23 @@ def gptq_dequant_matmul_gated(X: torch.Tensor, packed_gate: torch.Tensor, scales
                               scales_up: torch.Tensor, zeros_up: torch.Tensor,
                               perm: torch.Tensor | None, bits: int, group_size: int,
                               activation: str, Y: torch.Tensor, ws: torch.Tensor | None = None,
-                              stream=None) -> None:
+                              dev_status: torch.Tensor | None = None, stream=None) -> None:
     """Y = act(X Wg_hat^T) * (X Wu_hat^T) for a few tokens (decode form): two
     packed layers that share X, perm, bits and group_size; Y tokens x d_row
     bf16; ws as gptq_dequant_matmul_linear."""
-    _cuda(X, "X", torch.bfloat16)
-    ldx = _leading(X, "X")
+    dev = _first(X, "X")
     n_tok, d_col = X.shape
-    d_row = _packed_layer(X, "X", packed_gate, scales_gate, zeros_gate, bits, group_size, d_col, "_gate")
-    if _packed_layer(X, "X", packed_up, scales_up, zeros_up, bits, group_size, d_col, "_up") != d_row:
+    bits, group_size = int(bits), int(group_size)
+    p, s, z, d_row = _layer(packed_gate, scales_gate, zeros_gate, bits, group_size, d_col, dev, "_gate")
+    p2, s2, z2, d_up = _layer(packed_up, scales_up, zeros_up, bits, group_size, d_col, dev, "_up")
+    if d_up != d_row:
         raise ValueError("packed_gate and packed_up must have the same number of rows")
-    _order(X, "X", perm, d_col)
-    ldy = _rows(X, "X", Y, "Y", n_tok, d_row)
-    _same_device(X, "X", (ws, "ws", None))
-    _check(_lib.gptq_dequant_matmul_gated(_ptr(X), n_tok, d_col, ldx, _ptr(packed_gate),
-                                          _ptr(scales_gate), _ptr(zeros_gate), _ptr(packed_up),
-                                          _ptr(scales_up), _ptr(zeros_up), _ptr(perm), d_row,
-                                          int(bits), int(group_size), _activation(activation),
-                                          _ptr(Y), ldy, _ptr(ws), _bytes(ws), _stream(stream)),
-           "gptq_dequant_matmul_gated")
+    wsp, wsb = _buffer(ws, "ws", dev)
+    _check(_lib.gptq_dequant_matmul_gated(
+        X.data_ptr(), n_tok, d_col, _pitch(X, "X"), p, s, z, p2, s2, z2,
+        _whole(perm, "perm", _I32, (d_col,), dev), d_row, bits, group_size, _activation(activation),
+        _ptr(Y), _rows(Y, "Y", n_tok, d_row, dev), _status(dev_status, dev), wsp, wsb,
+        _launch_stream(stream, dev)), "gptq_dequant_matmul_gated")
 
 
 def gptq_dequant_matmul_gated_workspace_size(n_tok: int, d_col: int) -> int:
@@ -578,21 +608,17 @@ def gptq_dequant_gemm_linear(X: torch.Tensor, packed: torch.Tensor, scales: torc
     (W_hat as 16-bit weights): operands as gptq_dequant_matmul_linear; pre
     (tokens x d_row bf16), if given, receives the sums before the activation
     for the backward pass; ws of gptq_dequant_gemm_linear_workspace_size bytes."""
-    _cuda(X, "X", torch.bfloat16)
-    ldx = _leading(X, "X")
+    dev = _first(X, "X")
     n_tok, d_col = X.shape
-    d_row = _packed_layer(X, "X", packed, scales, zeros, bits, group_size, d_col)
-    _order(X, "X", perm, d_col)
-    _vector(X, "X", bias, "bias", d_row)
-    ldr = _rows(X, "X", residual, "residual", n_tok, d_row)
-    ldpre = _rows(X, "X", pre, "pre", n_tok, d_row)
-    ldy = _rows(X, "X", Y, "Y", n_tok, d_row)
-    _same_device(X, "X", (ws, "ws", None), (dev_status, "dev_status", torch.int32))
-    _check(_lib.gptq_dequant_gemm_linear(_ptr(X), n_tok, d_col, ldx, _ptr(packed), _ptr(scales),
-                                         _ptr(zeros), _ptr(perm), d_row, int(bits), int(group_size),
-                                         _ptr(bias), _activation(activation), _ptr(residual), ldr,
-                                         _ptr(pre), ldpre, _ptr(Y), ldy, _ptr(dev_status), _ptr(ws),
-                                         _bytes(ws), _stream(stream)), "gptq_dequant_gemm_linear")
+    bits, group_size = int(bits), int(group_size)
+    p, s, z, d_row = _layer(packed, scales, zeros, bits, group_size, d_col, dev)
+    wsp, wsb = _buffer(ws, "ws", dev)
+    _check(_lib.gptq_dequant_gemm_linear(
+        X.data_ptr(), n_tok, d_col, _pitch(X, "X"), p, s, z, _whole(perm, "perm", _I32, (d_col,), dev),
+        d_row, bits, group_size, _whole(bias, "bias", _F32, (d_row,), dev), _activation(activation),
+        _ptr(residual), _rows(residual, "residual", n_tok, d_row, dev), _ptr(pre),
+        _rows(pre, "pre", n_tok, d_row, dev), _ptr(Y), _rows(Y, "Y", n_tok, d_row, dev),
+        _status(dev_status, dev), wsp, wsb, _launch_stream(stream, dev)), "gptq_dequant_gemm_linear")
 
 
 def gptq_dequant_gemm_linear_workspace_size(n_tok: int, d_col: int, d_row: int) -> int:
@@ -610,24 +636,20 @@ def gptq_dequant_gemm_gated(X: torch.Tensor, packed_gate: torch.Tensor, scales_g
     both products, the activation and their product in one kernel; gate and
     up (tokens x d_row bf16), if given, receive the two products for the
     backward pass; ws of gptq_dequant_gemm_gated_workspace_size bytes."""
-    _cuda(X, "X", torch.bfloat16)
-    ldx = _leading(X, "X")
+    dev = _first(X, "X")
     n_tok, d_col = X.shape
-    d_row = _packed_layer(X, "X", packed_gate, scales_gate, zeros_gate, bits, group_size, d_col, "_gate")
-    if _packed_layer(X, "X", packed_up, scales_up, zeros_up, bits, group_size, d_col, "_up") != d_row:
+    bits, group_size = int(bits), int(group_size)
+    p, s, z, d_row = _layer(packed_gate, scales_gate, zeros_gate, bits, group_size, d_col, dev, "_gate")
+    p2, s2, z2, d_up = _layer(packed_up, scales_up, zeros_up, bits, group_size, d_col, dev, "_up")
+    if d_up != d_row:
         raise ValueError("packed_gate and packed_up must have the same number of rows")
-    _order(X, "X", perm, d_col)
-    ldg = _rows(X, "X", gate, "gate", n_tok, d_row)
-    ldu = _rows(X, "X", up, "up", n_tok, d_row)
-    ldy = _rows(X, "X", Y, "Y", n_tok, d_row)
-    _same_device(X, "X", (ws, "ws", None), (dev_status, "dev_status", torch.int32))
-    _check(_lib.gptq_dequant_gemm_gated(_ptr(X), n_tok, d_col, ldx, _ptr(packed_gate),
-                                        _ptr(scales_gate), _ptr(zeros_gate), _ptr(packed_up),
-                                        _ptr(scales_up), _ptr(zeros_up), _ptr(perm), d_row,
-                                        int(bits), int(group_size), _activation(activation),
-                                        _ptr(gate), ldg, _ptr(up), ldu, _ptr(Y), ldy,
-                                        _ptr(dev_status), _ptr(ws), _bytes(ws), _stream(stream)),
-           "gptq_dequant_gemm_gated")
+    wsp, wsb = _buffer(ws, "ws", dev)
+    _check(_lib.gptq_dequant_gemm_gated(
+        X.data_ptr(), n_tok, d_col, _pitch(X, "X"), p, s, z, p2, s2, z2,
+        _whole(perm, "perm", _I32, (d_col,), dev), d_row, bits, group_size, _activation(activation),
+        _ptr(gate), _rows(gate, "gate", n_tok, d_row, dev), _ptr(up), _rows(up, "up", n_tok, d_row, dev),
+        _ptr(Y), _rows(Y, "Y", n_tok, d_row, dev), _status(dev_status, dev), wsp, wsb,
+        _launch_stream(stream, dev)), "gptq_dequant_gemm_gated")
 
 
 def gptq_dequant_gemm_gated_workspace_size(n_tok: int, d_col: int, d_row: int) -> int:
@@ -647,23 +669,22 @@ def gptq_dequant_gemm_linear_backward(dY: torch.Tensor, packed: torch.Tensor, sc
     rows; may be None without an activation), dbias = its column sums (fp32,
     optional), dX = dPre W_hat (tokens x d_col bf16, original column order); ws
     of gptq_dequant_gemm_linear_backward_workspace_size bytes."""
-    _cuda(dY, "dY", torch.bfloat16)
-    lddy = _leading(dY, "dY")
+    dev = _first(dY, "dY")
     n_tok, d_row = dY.shape
-    _cuda(dX, "dX", torch.bfloat16)
+    if not isinstance(dX, _Tensor):
+        _refuse(dX, "dX", _BF16, dev)
     d_col = dX.shape[-1]
-    if _packed_layer(dY, "dY", packed, scales, zeros, bits, group_size, d_col) != d_row:
-        raise ValueError(f"packed must have dY's {d_row} columns as rows, got {packed.shape[0]}")
-    _order(dY, "dY", perm, d_col)
-    ldpre = _rows(dY, "dY", pre, "pre", n_tok, d_row)
-    lddp = _rows(dY, "dY", dPre, "dPre", n_tok, d_row)
-    _vector(dY, "dY", dbias, "dbias", d_row)
-    lddx = _rows(dY, "dY", dX, "dX", n_tok, d_col)
-    _same_device(dY, "dY", (ws, "ws", None), (dev_status, "dev_status", torch.int32))
+    bits, group_size = int(bits), int(group_size)
+    p, s, z, rows = _layer(packed, scales, zeros, bits, group_size, d_col, dev)
+    if rows != d_row:
+        raise ValueError(f"packed must have dY's {d_row} columns as rows, got {rows}")
+    wsp, wsb = _buffer(ws, "ws", dev)
     _check(_lib.gptq_dequant_gemm_linear_backward(
-        _ptr(dY), n_tok, d_row, lddy, _ptr(packed), _ptr(scales), _ptr(zeros), _ptr(perm), d_col,
-        int(bits), int(group_size), _activation(activation), _ptr(pre), ldpre, _ptr(dPre), lddp,
-        _ptr(dbias), _ptr(dX), lddx, _ptr(dev_status), _ptr(ws), _bytes(ws), _stream(stream)),
+        dY.data_ptr(), n_tok, d_row, _pitch(dY, "dY"), p, s, z, _whole(perm, "perm", _I32, (d_col,), dev),
+        d_col, bits, group_size, _activation(activation), _ptr(pre),
+        _rows(pre, "pre", n_tok, d_row, dev), _ptr(dPre), _rows(dPre, "dPre", n_tok, d_row, dev),
+        _whole(dbias, "dbias", _F32, (d_row,), dev), _ptr(dX), _rows(dX, "dX", n_tok, d_col, dev),
+        _status(dev_status, dev), wsp, wsb, _launch_stream(stream, dev)),
         "gptq_dequant_gemm_linear_backward")
 
 
@@ -685,28 +706,25 @@ def gptq_dequant_gemm_gated_backward(dY: torch.Tensor, gate: torch.Tensor, up: t
     (bf16, 16-byte aligned rows), dX = dGate Wg_hat + dUp Wu_hat (tokens x d_col
     bf16, original column order); ws of
     gptq_dequant_gemm_gated_backward_workspace_size bytes."""
-    _cuda(dY, "dY", torch.bfloat16)
-    lddy = _leading(dY, "dY")
+    dev = _first(dY, "dY")
     n_tok, d_row = dY.shape
-    _cuda(dX, "dX", torch.bfloat16)
+    if not isinstance(dX, _Tensor):
+        _refuse(dX, "dX", _BF16, dev)
     d_col = dX.shape[-1]
-    for packed, scales, zeros, suffix in ((packed_gate, scales_gate, zeros_gate, "_gate"),
-                                          (packed_up, scales_up, zeros_up, "_up")):
-        if _packed_layer(dY, "dY", packed, scales, zeros, bits, group_size, d_col, suffix) != d_row:
-            raise ValueError(f"packed{suffix} must have dY's {d_row} columns as rows, "
-                             f"got {packed.shape[0]}")
-    _order(dY, "dY", perm, d_col)
-    ldg = _rows(dY, "dY", gate, "gate", n_tok, d_row)
-    ldu = _rows(dY, "dY", up, "up", n_tok, d_row)
-    lddg = _rows(dY, "dY", dGate, "dGate", n_tok, d_row)
-    lddu = _rows(dY, "dY", dUp, "dUp", n_tok, d_row)
-    lddx = _rows(dY, "dY", dX, "dX", n_tok, d_col)
-    _same_device(dY, "dY", (ws, "ws", None), (dev_status, "dev_status", torch.int32))
+    bits, group_size = int(bits), int(group_size)
+    p, s, z, rows = _layer(packed_gate, scales_gate, zeros_gate, bits, group_size, d_col, dev, "_gate")
+    p2, s2, z2, rows2 = _layer(packed_up, scales_up, zeros_up, bits, group_size, d_col, dev, "_up")
+    if rows != d_row or rows2 != d_row:
+        raise ValueError(f"packed_gate and packed_up must have dY's {d_row} columns as rows, "
+                         f"got {rows} and {rows2}")
+    wsp, wsb = _buffer(ws, "ws", dev)
     _check(_lib.gptq_dequant_gemm_gated_backward(
-        _ptr(dY), n_tok, d_row, lddy, _ptr(gate), ldg, _ptr(up), ldu, _ptr(packed_gate),
-        _ptr(scales_gate), _ptr(zeros_gate), _ptr(packed_up), _ptr(scales_up), _ptr(zeros_up),
-        _ptr(perm), d_col, int(bits), int(group_size), _activation(activation), _ptr(dGate), lddg,
-        _ptr(dUp), lddu, _ptr(dX), lddx, _ptr(dev_status), _ptr(ws), _bytes(ws), _stream(stream)),
+        dY.data_ptr(), n_tok, d_row, _pitch(dY, "dY"), _ptr(gate),
+        _rows(gate, "gate", n_tok, d_row, dev), _ptr(up), _rows(up, "up", n_tok, d_row, dev),
+        p, s, z, p2, s2, z2, _whole(perm, "perm", _I32, (d_col,), dev), d_col, bits, group_size,
+        _activation(activation), _ptr(dGate), _rows(dGate, "dGate", n_tok, d_row, dev), _ptr(dUp),
+        _rows(dUp, "dUp", n_tok, d_row, dev), _ptr(dX), _rows(dX, "dX", n_tok, d_col, dev),
+        _status(dev_status, dev), wsp, wsb, _launch_stream(stream, dev)),
         "gptq_dequant_gemm_gated_backward")
 
 

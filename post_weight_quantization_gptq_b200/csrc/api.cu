@@ -326,14 +326,14 @@ gptq_status gptq_dequant_matmul_linear(const uint16_t* X, int64_t n_tok, int64_t
                                        const int32_t* zeros, const int32_t* perm, int64_t d_row,
                                        int32_t bits, int32_t group_size, const float* bias,
                                        int32_t activation, const uint16_t* residual, int64_t ldr,
-                                       uint16_t* Y, int64_t ldy, void* ws, size_t ws_bytes,
-                                       cudaStream_t stream) {
+                                       uint16_t* Y, int64_t ldy, int32_t* dev_status, void* ws,
+                                       size_t ws_bytes, cudaStream_t stream) {
     gptq_status c = check_packed(packed, scales, zeros);
     if (c == GPTQ_OK) c = check_shape(n_tok, d_col, d_row, bits, group_size, activation, perm);
     if (c != GPTQ_OK || n_tok == 0) return c;
     if (bad_rows(X, ldx, d_col) || bad_rows(Y, ldy, d_row)) return GPTQ_ERR_INVALID_ARG;
     if (residual != nullptr && bad_rows(residual, ldr, d_row)) return GPTQ_ERR_INVALID_ARG;
-    if (!aligned(bias, 4)) return GPTQ_ERR_INVALID_ARG;
+    if (!aligned(bias, 4) || !aligned(dev_status, 4)) return GPTQ_ERR_INVALID_ARG;
     if (gptq::needs_gather(X, ldx, perm) &&
         small_ws(ws, ws_bytes, gptq::linear_decode_workspace_bytes(n_tok, d_col)))
         return GPTQ_ERR_WORKSPACE;
@@ -342,7 +342,7 @@ gptq_status gptq_dequant_matmul_linear(const uint16_t* X, int64_t n_tok, int64_t
     a.mat[0] = {packed, scales, zeros};
     a.perm = perm; a.d_row = d_row; a.bits = bits; a.group = group_size;
     a.bias = bias; a.act = activation; a.residual = residual; a.ldr = ldr;
-    a.Y = Y; a.ldy = ldy; a.ws = ws;
+    a.Y = Y; a.ldy = ldy; a.status = dev_status; a.ws = ws;
     return launch_status(gptq::launch_linear_decode(a, stream));
 }
 
@@ -352,12 +352,14 @@ gptq_status gptq_dequant_matmul_gated(const uint16_t* X, int64_t n_tok, int64_t 
                                       const float* scales_up, const int32_t* zeros_up,
                                       const int32_t* perm, int64_t d_row, int32_t bits,
                                       int32_t group_size, int32_t activation, uint16_t* Y,
-                                      int64_t ldy, void* ws, size_t ws_bytes, cudaStream_t stream) {
+                                      int64_t ldy, int32_t* dev_status, void* ws, size_t ws_bytes,
+                                      cudaStream_t stream) {
     gptq_status c = check_packed(packed_gate, scales_gate, zeros_gate);
     if (c == GPTQ_OK) c = check_packed(packed_up, scales_up, zeros_up);
     if (c == GPTQ_OK) c = check_shape(n_tok, d_col, d_row, bits, group_size, activation, perm);
     if (c != GPTQ_OK || n_tok == 0) return c;
     if (bad_rows(X, ldx, d_col) || bad_rows(Y, ldy, d_row)) return GPTQ_ERR_INVALID_ARG;
+    if (!aligned(dev_status, 4)) return GPTQ_ERR_INVALID_ARG;
     if (gptq::needs_gather(X, ldx, perm) &&
         small_ws(ws, ws_bytes, gptq::linear_decode_workspace_bytes(n_tok, d_col)))
         return GPTQ_ERR_WORKSPACE;
@@ -366,7 +368,7 @@ gptq_status gptq_dequant_matmul_gated(const uint16_t* X, int64_t n_tok, int64_t 
     a.mat[0] = {packed_gate, scales_gate, zeros_gate};
     a.mat[1] = {packed_up, scales_up, zeros_up};
     a.perm = perm; a.d_row = d_row; a.bits = bits; a.group = group_size;
-    a.act = activation; a.Y = Y; a.ldy = ldy; a.ws = ws;
+    a.act = activation; a.Y = Y; a.ldy = ldy; a.status = dev_status; a.ws = ws;
     return launch_status(gptq::launch_linear_decode(a, stream));
 }
 

@@ -138,6 +138,16 @@ __device__ __forceinline__ void tma_load_2d(void* smem_dst, const void* tmap, ui
         : "memory");
 }
 
+// the same with the destination as a shared-memory address
+__device__ __forceinline__ void tma_load_2d_at(uint32_t smem_dst, const void* tmap, uint64_t* bar,
+                                               int32_t c0, int32_t c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
+        : "memory");
+}
+
 // ---------------------------------------------------------------- tcgen05
 // Tensor-memory allocation (whole warp).  The allocated base address is
 // written to *dst in shared memory.

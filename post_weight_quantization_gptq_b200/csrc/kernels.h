@@ -47,9 +47,10 @@ inline cudaError_t launch_kernel(bool pdl, void (*kern)(KArgs...), dim3 grid, di
     return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
 }
 
-// Shared-memory swizzle of a TMA box: none, 128-byte (16-byte chunks), or
-// 128-byte with 32-byte chunks (the layout 32-bit MN-major MMA operands use).
-enum class Swz { kNone, k128, k128Atom32 };
+// Shared-memory swizzle of a TMA box: none, 32-, 64- or 128-byte (16-byte
+// chunks), or 128-byte with 32-byte chunks (the layout 32-bit MN-major MMA
+// operands use).
+enum class Swz { kNone, k32, k64, k128, k128Atom32 };
 
 // 2-D TMA tensor map over a row-major matrix of `outer` rows x `inner`
 // columns (leading dimension ld_elems), boxes of box_outer x box_inner

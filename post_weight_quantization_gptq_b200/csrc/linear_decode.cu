@@ -4,28 +4,37 @@
 // with W[n][k] = s[k/g][n] (q[n][k] - z[k/g][n]) in fp32, Y rounded once to bf16.
 //
 // Mathematics.  Per group the scale and zero point leave the sum,
-//   sum_k x_k s (q_k - z) = s ( sum_k x_k (c + q_k) - (c + z) sum_k x_k ),
-// and c + q_k is built without a conversion: a code's bits ORed into the
-// mantissa of bf16 128 (0x4300, one unit per code step) give 128 + q exactly;
-// an 8-bit code is two of them, 128 + its low half and 2048 + 16 its high half
-// (0x4500, steps of 16).  The sums run on the tensor cores (m16n8k16, 16 weight
-// rows by 8 tokens, exact products of bf16 values, fp32 sums), the plain token
-// sum through one more tile of ones, whose result lands in the registers that
-// need it.  c <= 2176 costs log2(c / |q - z|) bits of the 24, far below the
-// output's 8.
+//   sum_k x_k s (q_k - z) = s ( sum_k x_k q_k - z sum_k x_k ),
+// and a code needs no conversion: the bf16 bit patterns 0 .. 255 are the
+// numbers p 2^-133 (subnormal, then the first binade, evenly spaced), so a
+// code masked out of its word, wherever in the low byte of a half word it
+// lies, is q 2^(j - 133) for its bit position j.  The tokens are multiplied by
+// 2^(64 - j) to match (exact), which keeps the sums, 2^-69 of the result, in
+// fp32's normal range; the result is scaled back at the end.  The sums run on
+// the tensor cores (m16n8k16, 16 weight rows by 8 tokens, exact products,
+// fp32 sums), the plain token sum through one more tile whose codes are all 1,
+// so that it lands in the registers that need it.  Tokens of magnitude 2^63
+// and more overflow; below 2^-57 the products lose relative precision (2^-80
+// absolute).
 //
 // Bound: the packed layer is read once for up to 32 tokens, so HBM; below
-// about 10 MB the launch and the length of one warp's chain.  Which 16 codes meet in an instruction
-// is free as long as X agrees, so a lane reads 32 consecutive codes of a row
-// in one or two vector loads (the lanes of a row 128 codes together) and
-// needs 7 shift / logic instructions per 8 codes.
+// about 10 MB the launch and the length of one warp's chain.  What costs after
+// that is issue slots: at the measured copy rate an SM receives 46 4-bit codes
+// per cycle, 2.8 thread instructions each.  Which 16 codes meet in an
+// instruction is free as long as the tokens agree, so a lane takes 8
+// consecutive codes of two rows and masks them out with 5 shift / logic
+// instructions (7 where each pair is brought to the low bits and completed to
+// 128 + q); weights and tokens arrive by TMA, which costs the warps nothing
+// (per-thread asynchronous copies took 258 of 448 instructions per 4096 codes).
 //
-// Work split: a warp owns 32 weight rows (gated: 16 of each matrix) and every
-// kth block of 128 codes; the warps of a CTA, and of a cluster of CTAs, split
-// K so that a layer of few rows still fills the GPU.  Partial sums meet in
-// shared memory, across the cluster through distributed shared memory, in a
-// fixed order (no atomics).  More tokens put more warps on different rows of
-// one CTA, which share the tokens' loads in L1.
+// Work split: a warp owns 16 MT weight rows (gated: half of them of each
+// matrix) and every kth block of 128 codes, with a ring of blocks of its own in
+// shared memory that its lane 0 refills -- no barrier between warps, no
+// producer.  The warps of a CTA, and of a cluster of CTAs, split K so that a
+// layer of few rows still fills the GPU.  Partial sums meet in shared memory,
+// across the cluster through distributed shared memory, in a fixed order (no
+// atomics).  Every wait is bounded (GPTQ_ERR_TIMEOUT).
+#include <cuda.h>
 #include <cooperative_groups.h>
 
 #include "activation.cuh"
@@ -39,9 +48,10 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kTiles = 2;            // 16-row weight tiles per warp
 constexpr int kBlock = 128;          // codes per row and step of a warp
 constexpr int kMaxTok = 32;          // tokens per launch
+constexpr int kMaxDepth = 8;         // blocks of a warp's ring
+constexpr int kSmemTwo = 112 * 1024, kSmemOne = 224 * 1024;   // for two and one CTA per SM
 
 // How groups lie in a block of 128 codes: a block lies in one group; a group
 // is 32 or 64 codes; a group is 8 or 16 codes.
@@ -49,350 +59,464 @@ enum GroupMode { kWide, kNarrow, kTiny };
 
 struct Args {
     PackedMatrix mat[2];
-    const uint16_t* X;   // quantization order, rows 16-byte aligned
-    int64_t ldx;
     int n_tok, K, N, g;
-    int64_t words;       // packed words per row
     const float* bias;
     const uint16_t* residual;
     int64_t ldr;
     uint16_t* Y;
     int64_t ldy;
     int act;
+    int gathered;            // the tokens are written by the kernel launched just before
+    int depth;               // blocks of the ring
+    int slot_bytes;          // of one: weights, then tokens
+    int ngb_log2;            // groups per block (kNarrow, kTiny)
+    int blocks_per_group;    // (kWide)
+    uint32_t group_magic;    // block / blocks_per_group = high word of block * group_magic; 0: divide
+    int32_t* status;
 };
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// A token row's 16 bytes.  Coherent (the gather before this kernel may still
-// run when it starts) and cached in L1 (other warps of the CTA read them too).
-__device__ __forceinline__ uint4 load_x(const uint16_t* p) {
-    uint4 v;
-    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
-
-// A lane's 32 consecutive codes of one row (BITS words).
-template <int BITS>
-__device__ __forceinline__ void load_codes(const uint32_t* p, uint32_t (&w)[BITS]) {
-    if constexpr (BITS == 2) {
-        const uint2 v = __ldcs(reinterpret_cast<const uint2*>(p));
-        w[0] = v.x; w[1] = v.y;
-    } else if constexpr (BITS == 3) {
-        w[0] = __ldcs(p); w[1] = __ldcs(p + 1); w[2] = __ldcs(p + 2);
-    } else {
-#pragma unroll
-        for (int q = 0; q < BITS / 4; ++q) {
-            const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p) + q);
-            w[4 * q] = v.x; w[4 * q + 1] = v.y; w[4 * q + 2] = v.z; w[4 * q + 3] = v.w;
-        }
-    }
-}
-
-// Eight consecutive codes (a unit) as the words the pair extraction reads:
-// code i's bits at STEP * i of the low half, code i + 4's of the high half
-// (8-bit codes keep two words, codes 0..3 and 4..7).
+// Eight consecutive codes (a unit): one word, two at 8 bits.  The words of
+// three and two bits hold codes 0..3 from bit 0 and codes 4..7 from bit 16.
 template <int BITS>
 struct Unit {
     uint32_t v[BITS == 8 ? 2 : 1];
 };
 
+// Where unit 4j + t lies in the 128 codes of a row: a byte offset from the
+// start of row 0 of an 8-row group (16 BITS bytes per row, groups on 1024-byte
+// boundaries or, at 3 bits, anywhere).  The copy's swizzle permutes a row's
+// 16-byte pieces by its number, so that the 32 lanes' reads (rows g8 = 0..7,
+// t = 0..3) meet 32 banks.
 template <int BITS>
-__device__ __forceinline__ Unit<BITS> unit_of(const uint32_t (&w)[BITS], int j) {
+__device__ __forceinline__ uint32_t unit_offset(int j, int g8, int t) {
+    if constexpr (BITS == 4) return g8 * 64 + ((j ^ (g8 >> 1)) << 4) + 4 * t;                        // 64-byte swizzle
+    else if constexpr (BITS == 2) return g8 * 32 + (((j >> 1) ^ (g8 >> 2)) << 4) + 8 * (j & 1) + 2 * t;  // 32-byte
+    else if constexpr (BITS == 3) return g8 * 48 + 12 * j + 4 * ((3 * t) >> 2);                      // none
+    else return g8 * 128 + (((2 * j + (t >> 1)) ^ g8) << 4) + 8 * (t & 1);                           // 128-byte
+}
+template <int BITS>
+__device__ __forceinline__ Unit<BITS> load_unit(const uint8_t* at, int t) {
     Unit<BITS> u;
     if constexpr (BITS == 4) {
-        u.v[0] = w[j];
+        u.v[0] = *reinterpret_cast<const uint32_t*>(at);
     } else if constexpr (BITS == 2) {
-        u.v[0] = __byte_perm(w[j >> 1], 0, (j & 1) ? 0x4342 : 0x4140);
-    } else if constexpr (BITS == 3) {
-        const uint32_t b = j == 0 ? w[0]
-                         : j == 1 ? __funnelshift_r(w[0], w[1], 24)
-                         : j == 2 ? __funnelshift_r(w[1], w[2], 16) : (w[2] >> 8);
-        u.v[0] = (b & 0xFFFu) | ((b & 0xFFF000u) << 4);
+        u.v[0] = __byte_perm(*reinterpret_cast<const uint16_t*>(at), 0, 0x4140);
+    } else if constexpr (BITS == 3) {   // 24 bits of two words (the fourth unit: of one)
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(at);
+        const uint32_t v = __funnelshift_r(w[0], w[t == 3 ? 0 : 1], (24 * t) & 31);
+        u.v[0] = __byte_perm(v, v << 4, 0x7610);
     } else {
-        u.v[0] = w[2 * j];
-        u.v[1] = w[2 * j + 1];
+        const uint2 v = *reinterpret_cast<const uint2*>(at);
+        u.v[0] = v.x;
+        u.v[1] = v.y;
     }
     return u;
 }
 
-// Codes i and i + 4 of the unit as bf16 128 + q (8 bits: 128 + the low half;
-// the high half as 2048 + 16 h by pair_high).
+// The unit's codes as four words of two bf16 patterns: word i holds codes i and
+// i + 4 (8 bits: words 0, 1 codes 0 | 2 and 1 | 3, words 2, 3 codes 4 | 6 and
+// 5 | 7), at bit position shift_of(i) of the half words.
 template <int BITS>
-__device__ __forceinline__ uint32_t pair_low(const Unit<BITS>& u, int i) {
+__device__ __forceinline__ uint32_t pair_of(const Unit<BITS>& u, int i) {
     if constexpr (BITS == 8) {
-        const uint32_t p = __byte_perm(u.v[0], u.v[1], 0x0400 + 0x0101 * i);
-        return (p & 0x000F000Fu) | 0x43004300u;
+        return (i & 1) ? __byte_perm(u.v[i >> 1], 0, 0x4341) : (u.v[i >> 1] & 0x00FF00FFu);
+    } else if constexpr (BITS == 2) {
+        return u.v[0] & (0x00030003u << (2 * i));
     } else {
-        constexpr uint32_t kMask = ((1u << BITS) - 1u) * 0x00010001u;
-        return ((u.v[0] >> (BITS * i)) & kMask) | 0x43004300u;
+        // two codes fit the low byte: the upper pairs after one shift
+        const uint32_t v = i < 2 ? u.v[0] : u.v[0] >> (2 * BITS);
+        return v & (((1u << BITS) - 1u) * 0x00010001u << (i & 1 ? BITS : 0));
     }
 }
-__device__ __forceinline__ uint32_t pair_high(const Unit<8>& u, int i) {
-    const uint32_t p = __byte_perm(u.v[0], u.v[1], 0x0400 + 0x0101 * i);
-    return ((p >> 4) & 0x000F000Fu) | 0x45004500u;
+template <int BITS>
+__host__ __device__ constexpr int shift_of(int i) {
+    return BITS == 8 ? 0 : BITS == 2 ? 2 * i : (i & 1) * BITS;
+}
+// 2^e as a pair of bf16
+__host__ __device__ constexpr uint32_t bf16x2_pow2(int e) { return static_cast<uint32_t>(127 + e) << 7 | static_cast<uint32_t>(127 + e) << 23; }
+constexpr int kScaleUp = 64;                 // of the tokens
+constexpr float kScaleBack = 0x1p69f;        // 2^(133 - 64)
+
+// Eight consecutive token values as the four words that meet the unit's.
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+template <int BITS>
+__device__ __forceinline__ void token_pairs(uint4 v, uint32_t (&x)[4]) {
+    if constexpr (BITS == 8) {
+        x[0] = __byte_perm(v.x, v.y, 0x5410);
+        x[1] = __byte_perm(v.x, v.y, 0x7632);
+        x[2] = __byte_perm(v.z, v.w, 0x5410);
+        x[3] = __byte_perm(v.z, v.w, 0x7632);
+    } else {
+        x[0] = __byte_perm(v.x, v.z, 0x5410);
+        x[1] = __byte_perm(v.x, v.z, 0x7632);
+        x[2] = __byte_perm(v.y, v.w, 0x5410);
+        x[3] = __byte_perm(v.y, v.w, 0x7632);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = mul_bf16x2(x[i], bf16x2_pow2(kScaleUp - shift_of<BITS>(i)));
 }
 
-// Lane t of a quad holds units 4t .. 4t+3; afterwards unit 4j + t for j = 0..3
-// (a 4 x 4 transposition across the quad in two exchange steps).
-template <int W>
-__device__ __forceinline__ void quad_transpose(uint32_t (&v)[4][W], int t) {
-#pragma unroll
-    for (int x = 0; x < W; ++x) {
-#pragma unroll
-        for (int j = 0; j < 4; j += 2) {
-            const uint32_t send = (t & 1) ? v[j][x] : v[j + 1][x];
-            const uint32_t got = __shfl_xor_sync(0xffffffffu, send, 1);
-            if (t & 1) v[j][x] = got; else v[j + 1][x] = got;
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const uint32_t send = (t & 2) ? v[j][x] : v[j + 2][x];
-            const uint32_t got = __shfl_xor_sync(0xffffffffu, send, 2);
-            if (t & 2) v[j][x] = got; else v[j + 2][x] = got;
-        }
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool in) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// all but the newest n groups of this thread have landed
+__device__ __forceinline__ void cp_wait(int n) {
+    switch (n) {
+        case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+        case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+        case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+        case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+        case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+        case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+        case 6: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
+        default: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;
     }
 }
 
-// WR: row groups of a CTA (its other warps split K).  Cluster ranks (y) split K too.
-template <int BITS, int MODE, int NT, bool GATED, int WR>
-__global__ void __launch_bounds__(kThreads, NT >= 4 || (BITS == 8 && NT >= 2) ? 1 : 2)
-    decode_kernel(const Args a) {
-    constexpr int WK = kWarps / WR;
-    constexpr int kRows = 16 * kTiles * WR;         // weight rows of the CTA
+// NT tiles of 8 tokens, MT tiles of 16 weight rows per warp.
+template <int BITS, int NT, int MT>
+struct Shape {
+    static constexpr int kRows = 16 * MT;                    // weight rows of the CTA
+    static constexpr int kRowBytes = 16 * BITS;              // 128 codes
+    static constexpr int kWBytes = kRows * kRowBytes;        // of a block
+    static constexpr int kPitch = kRows + 4;                 // of the partial sums
+    static constexpr int kRedBytes = kWarps * 8 * NT * kPitch * 4;
+    static constexpr int kHead = 1024;                       // barriers
+};
+
+template <int BITS, int MODE, int NT, int MT, bool GATED>
+__global__ void __launch_bounds__(kThreads, NT * MT >= 8 ? 1 : 2)
+    decode_kernel(const __grid_constant__ CUtensorMap tmw0, const __grid_constant__ CUtensorMap tmw1,
+                  const __grid_constant__ CUtensorMap tmx, const __grid_constant__ Args a) {
+    using S = Shape<BITS, NT, MT>;
+    constexpr int kRows = S::kRows;
     constexpr int kTok = 8 * NT;
-    constexpr int kPitch = kRows + 4;
-    constexpr float kOff = BITS == 8 ? 2176.f : 128.f;
-    __shared__ float red[WK][kTok][kPitch];
+    constexpr int kTilesM = GATED ? MT / 2 : MT;             // tiles of one matrix
+    constexpr int kOut = 16 * kTilesM;                       // outputs of the CTA
+    extern __shared__ __align__(1024) uint8_t sm[];
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm);        // [kWarps][kMaxDepth]
+    int* abort_word = reinterpret_cast<int*>(bars + kWarps * kMaxDepth);
+    volatile int* abort = abort_word;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int wr = warp % WR, wk = warp / WR;
     const int g8 = lane >> 2, t = lane & 3;
-    const int n0 = blockIdx.x * (GATED ? 16 * WR : kRows);   // the CTA's first output
+    const int n0 = blockIdx.x * kOut;
     const int ranks = gridDim.y, rank = blockIdx.y;
     const int nblk = (a.K + kBlock - 1) / kBlock;
-    const int step = WK * ranks;
+    const int first = rank * kWarps + warp, stride = ranks * kWarps;
+    const int steps = nblk > first ? (nblk - first + stride - 1) / stride : 0;   // blocks of this warp
+    const int depth = a.depth;
+    const int ngb_log2 = MODE == kWide ? 0 : a.ngb_log2;     // groups per block
+    const int groups = (a.K + a.g - 1) / a.g;
+    uint64_t* full = bars + warp * kMaxDepth;
+    const int half_bytes = a.n_tok * 128;                    // 64 codes of the tokens
+    const uint8_t* ring_p = sm + S::kHead + warp * depth * a.slot_bytes;
+    const uint32_t ring = smem_u32(ring_p);
+    const int sc_bytes = 2 * kRows * 4 << ngb_log2;          // a block's scales, then zero points
+    uint8_t* sc_ring = sm + S::kHead + kWarps * depth * a.slot_bytes + warp * depth * sc_bytes;
 
-    // the lane's rows: tile m, row g8 and g8 + 8 (clamped: surplus rows are
-    // computed from the last row and dropped)
-    const uint32_t* base[kTiles][2];
-    int row[kTiles][2];
-#pragma unroll
-    for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int r = GATED ? n0 + 16 * wr + g8 + 8 * h : n0 + 32 * wr + 16 * m + g8 + 8 * h;
-            row[m][h] = min(r, a.N - 1);
-            base[m][h] = a.mat[GATED ? m : 0].packed + row[m][h] * a.words + t * BITS;
+    // lane 0: a block's weights, and its tokens
+    auto load_weights = [&](int s, int slot) {
+        const int x = (first + s * stride) * (4 * BITS);
+        const uint32_t dst = ring + slot * a.slot_bytes;
+        mbar_arrive_expect_tx(&full[slot], S::kWBytes + 2 * half_bytes);
+        if constexpr (GATED) {
+            tma_load_2d_at(dst, &tmw0, &full[slot], x, n0);
+            tma_load_2d_at(dst + S::kWBytes / 2, &tmw1, &full[slot], x, n0);
+        } else {
+            tma_load_2d_at(dst, &tmw0, &full[slot], x, n0);
         }
-
-    float acc[kTiles][NT][4];
+    };
+    auto load_tokens = [&](int s, int slot) {
+        const int x = (first + s * stride) * kBlock;
+        const uint32_t dst = ring + slot * a.slot_bytes + S::kWBytes;
+        tma_load_2d_at(dst, &tmx, &full[slot], x, 0);
+        tma_load_2d_at(dst + half_bytes, &tmx, &full[slot], x + 64, 0);
+    };
+    // the warp: the scales and zero points of a block's groups, [group][row]
+    // (4 bytes each: their rows in memory have any alignment)
+    constexpr int kOwn = (kRows + 31) / 32;                  // rows per lane
+    const float* sc_src[kOwn];
+    int64_t z_off[kOwn];                                     // bytes from there to the zero point
+    bool live[kOwn];
 #pragma unroll
-    for (int m = 0; m < kTiles; ++m)
+    for (int i = 0; i < kOwn; ++i) {
+        const int r = lane + 32 * i, n = n0 + r % kOut;
+        const PackedMatrix& m = a.mat[GATED && r >= kOut ? 1 : 0];
+        live[i] = r < kRows && n < a.N;
+        sc_src[i] = m.scales + (live[i] ? n : 0);
+        z_off[i] = reinterpret_cast<const char*>(m.zeros) - reinterpret_cast<const char*>(m.scales);
+    }
+    auto load_scales = [&](int b, int slot) {
+        const uint32_t dst = smem_u32(sc_ring) + slot * sc_bytes + 4 * lane;
+        for (int q = 0; q < (1 << ngb_log2); ++q) {
+            // kWide: block / blocks per group, as a multiplication where that is exact
+            const int gi = MODE != kWide ? (b << ngb_log2) + q
+                         : a.group_magic != 0 ? static_cast<int>(__umulhi(b, a.group_magic)) : b / a.blocks_per_group;
+            const int64_t off = static_cast<int64_t>(gi) * a.N;
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i) {
+                const bool in = live[i] && gi < groups;
+                const char* src = reinterpret_cast<const char*>(sc_src[i] + (in ? off : 0));
+                if (kRows % 32 == 0 || lane + 32 * i < kRows) {
+                    cp4(dst + 4 * (q * kRows + 32 * i), src, in);
+                    cp4(dst + 4 * (q * kRows + 32 * i) + sc_bytes / 2, src + z_off[i], in);
+                }
+            }
+        }
+    };
+
+    if (lane == 0) {
+        for (int d = 0; d < depth; ++d) mbar_init(&full[d], 1);
+        if (warp == 0) *abort_word = 0;
+        fence_barrier_init();
+        fence_async_smem();
+        if (warp == 0) {
+            tma_prefetch_desc(&tmw0);
+            tma_prefetch_desc(&tmx);
+        }
+        // a warp's barriers are its own: its copies need not wait for the others
+        for (int d = 0; d < depth && d < steps; ++d) {
+            load_weights(d, d);
+            if (!a.gathered) load_tokens(d, d);
+        }
+    }
+    for (int d = 0; d < depth; ++d) {
+        if (d < steps) load_scales(first + d * stride, d);
+        cp_commit();
+    }
+    if (a.gathered) {
+        pdl_wait();   // the tokens come from the kernel before; weights and scales do not
+        if (lane == 0)
+            for (int d = 0; d < depth && d < steps; ++d) load_tokens(d, d);
+    }
+    __syncthreads();   // the abort word is set up
+
+    float acc[MT][NT][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int q = 0; q < NT; ++q)
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[m][q][i] = 0.f;
 
-    uint32_t nxt[kTiles][2][BITS];
-    auto fetch = [&](int b) {
-        const bool in = b < nblk && b * kBlock + 32 * t < a.K;
+    // Where a lane reads in a slot (slots lie on 1024-byte boundaries).  Column
+    // g8 of a token tile stands for token (g8 >> 1) | (g8 & 1) << 2, so that
+    // neighbouring columns are four rows apart, which the copy's 128-byte
+    // swizzle puts half the banks away; a column past the last token repeats
+    // that and is dropped.
+    uint32_t w_off[4], x_off[NT][4];
 #pragma unroll
-        for (int m = 0; m < kTiles; ++m)
+    for (int j = 0; j < 4; ++j) {
+        w_off[j] = unit_offset<BITS>(j, g8, t);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (in) {
-                    load_codes<BITS>(base[m][h] + static_cast<int64_t>(b) * (4 * BITS), nxt[m][h]);
-                } else {
+        for (int q = 0; q < NT; ++q) {
+            const int tok = min(8 * q + ((g8 >> 1) | (g8 & 1) << 2), a.n_tok - 1);
+            const uint32_t at = S::kWBytes + (j >> 1) * half_bytes + tok * 128;
+            x_off[q][j] = at + (((4 * (j & 1) + t) ^ ((at >> 7) & 7)) << 4);
+        }
+    }
+
+    int slot = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    int done = 0;
+    for (int s = 0; s < steps; ++s) {
+        if (!mbar_wait(&full[slot], phase, abort)) {
+            ok = false;
+            done = s;
+            break;
+        }
+        cp_wait(depth - 1);
+        __syncwarp();
+        const int b = first + s * stride;
+        const uint8_t* at = ring_p + slot * a.slot_bytes;
+
+        // c += the 32 codes of step j of tile m times the tokens; `mask` keeps
+        // this lane's codes (all ones) or drops them (a group of 8 or 16 codes)
+        auto units = [&](int m, int j, Unit<BITS> (&u)[2]) {
+            u[0] = load_unit<BITS>(at + w_off[j] + 16 * m * S::kRowBytes, t);
+            u[1] = load_unit<BITS>(at + w_off[j] + (16 * m + 8) * S::kRowBytes, t);
+        };
+        auto product = [&](const Unit<BITS> (&u)[2], const uint32_t (&xb)[NT][4], uint32_t mask, float (&c)[NT][4]) {
 #pragma unroll
-                    for (int i = 0; i < BITS; ++i) nxt[m][h][i] = 0;
-                }
+            for (int p = 0; p < 4; p += 2) {
+                const uint32_t a0 = pair_of<BITS>(u[0], p) & mask, a1 = pair_of<BITS>(u[1], p) & mask;
+                const uint32_t a2 = pair_of<BITS>(u[0], p + 1) & mask, a3 = pair_of<BITS>(u[1], p + 1) & mask;
+#pragma unroll
+                for (int q = 0; q < NT; ++q) mma_bf16(c[q], a0, a1, a2, a3, xb[q][p], xb[q][p + 1]);
             }
-    };
-    const int blocks_per_group = a.g / kBlock;   // kWide with more than one group
-    int b = rank * WK + wk;
-    fetch(b);
-    pdl_wait();   // X may come from the gather launched before this kernel
-
-    for (; b < nblk; b += step) {
-        uint32_t cur[kTiles][2][BITS];
+        };
+        // the same with codes of 1
+        auto total = [&](const uint32_t (&xb)[NT][4], uint32_t mask, float (&c)[NT][4]) {
 #pragma unroll
-        for (int m = 0; m < kTiles; ++m)
+            for (int p = 0; p < 4; p += 2) {
+                const uint32_t o0 = (0x00010001u << shift_of<BITS>(p)) & mask;
+                const uint32_t o1 = (0x00010001u << shift_of<BITS>(p + 1)) & mask;
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int i = 0; i < BITS; ++i) cur[m][h][i] = nxt[m][h][i];
-        fetch(b + step);
-
-        constexpr int UW = BITS == 8 ? 2 : 1;
-        uint32_t un[kTiles][2][4][UW];
-#pragma unroll
-        for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const Unit<BITS> u = unit_of<BITS>(cur[m][h], j);
-#pragma unroll
-                    for (int x = 0; x < UW; ++x) un[m][h][j][x] = u.v[x];
-                }
-                if constexpr (MODE != kWide) quad_transpose<UW>(un[m][h], t);
+                for (int q = 0; q < NT; ++q) mma_bf16(c[q], o0, o0, o1, o1, xb[q][p], xb[q][p + 1]);
             }
-
-        float c[kTiles][NT][4], cs[NT][4];
-        auto clear = [&]() {
+        };
+        auto clear = [&](float (&c)[NT][4]) {
 #pragma unroll
             for (int q = 0; q < NT; ++q)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    cs[q][i] = 0.f;
-#pragma unroll
-                    for (int m = 0; m < kTiles; ++m) c[m][q][i] = 0.f;
-                }
+                for (int i = 0; i < 4; ++i) c[q][i] = 0.f;
         };
-        // the 32 codes that step j of the quad covers; `mask` keeps this
-        // lane's codes (all ones) or drops them (a group of 8 or 16 codes)
-        auto products = [&](int j, const uint32_t (&xb)[NT][4], uint32_t mask) {
-            const uint32_t one = 0x3F803F80u & mask;
+        // the finished sums of tile m and the block's group enter the outputs
+        const float* sc = reinterpret_cast<const float*>(sc_ring + slot * sc_bytes) + g8;
+        const int32_t* zc = reinterpret_cast<const int32_t*>(sc) + (kRows << ngb_log2);
+        auto fold = [&](int m, int grp, const float (&c)[NT][4], const float (&cs)[NT][4]) {
 #pragma unroll
-            for (int m = 0; m < kTiles; ++m) {
-                Unit<BITS> u0, u1;
+            for (int h = 0; h < 2; ++h) {
+                const float sv = sc[grp * kRows + m * 16 + 8 * h];
+                const float z = static_cast<float>(zc[grp * kRows + m * 16 + 8 * h]);
 #pragma unroll
-                for (int x = 0; x < UW; ++x) {
-                    u0.v[x] = un[m][0][j][x];
-                    u1.v[x] = un[m][1][j][x];
-                }
+                for (int q = 0; q < NT; ++q)
 #pragma unroll
-                for (int p = 0; p < 4; p += 2) {
-                    const uint32_t a0 = pair_low<BITS>(u0, p) & mask, a1 = pair_low<BITS>(u1, p) & mask;
-                    const uint32_t a2 = pair_low<BITS>(u0, p + 1) & mask, a3 = pair_low<BITS>(u1, p + 1) & mask;
-#pragma unroll
-                    for (int q = 0; q < NT; ++q) mma_bf16(c[m][q], a0, a1, a2, a3, xb[q][p], xb[q][p + 1]);
-                    if constexpr (BITS == 8) {
-                        const uint32_t h0 = pair_high(u0, p) & mask, h1 = pair_high(u1, p) & mask;
-                        const uint32_t h2 = pair_high(u0, p + 1) & mask, h3 = pair_high(u1, p + 1) & mask;
-#pragma unroll
-                        for (int q = 0; q < NT; ++q) mma_bf16(c[m][q], h0, h1, h2, h3, xb[q][p], xb[q][p + 1]);
-                    }
-                }
+                    for (int i = 0; i < 2; ++i)
+                        acc[m][q][2 * h + i] = fmaf(sv, fmaf(-z, cs[q][i], c[q][2 * h + i]), acc[m][q][2 * h + i]);
             }
-#pragma unroll
-            for (int q = 0; q < NT; ++q)
-#pragma unroll
-                for (int p = 0; p < 4; p += 2) mma_bf16(cs[q], one, one, one, one, xb[q][p], xb[q][p + 1]);
         };
-        // the finished group's sums enter the outputs
-        auto fold = [&](int group) {
-#pragma unroll
-            for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const PackedMatrix& mt = a.mat[GATED ? m : 0];
-                    const int64_t at = static_cast<int64_t>(group) * a.N + row[m][h];
-                    const float s = __ldg(mt.scales + at);
-                    const float z = kOff + static_cast<float>(__ldg(mt.zeros + at));
-#pragma unroll
-                    for (int q = 0; q < NT; ++q)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            acc[m][q][2 * h + i] = fmaf(s, fmaf(-z, cs[q][i], c[m][q][2 * h + i]), acc[m][q][2 * h + i]);
-                }
-        };
-        // the tokens' values of step j, paired like the codes
+        // the tokens' values of step j (unit 4j + t), paired like the codes
         auto tokens = [&](int j, uint32_t (&xb)[NT][4]) {
-            const int k = b * kBlock + 8 * (MODE == kWide ? 4 * t + j : 4 * j + t);
 #pragma unroll
             for (int q = 0; q < NT; ++q) {
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (8 * q + g8 < a.n_tok && k < a.K) v = load_x(a.X + (8 * q + g8) * a.ldx + k);
-                xb[q][0] = __byte_perm(v.x, v.z, 0x5410);
-                xb[q][1] = __byte_perm(v.x, v.z, 0x7632);
-                xb[q][2] = __byte_perm(v.y, v.w, 0x5410);
-                xb[q][3] = __byte_perm(v.y, v.w, 0x7632);
+                const uint4 v = *reinterpret_cast<const uint4*>(at + x_off[q][j]);
+                token_pairs<BITS>(v, xb[q]);
             }
         };
+        const int left = a.K - b * kBlock;   // codes from this block on
 
-        if constexpr (MODE == kWide) {
-            clear();
+        if constexpr (MODE == kTiny) {
+            // groups of 8 or 16: the lanes of a quad hold different ones
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
+                if (32 * j >= left) break;   // the same for every lane
                 uint32_t xb[NT][4];
                 tokens(j, xb);
-                products(j, xb, 0xffffffffu);
-            }
-            fold(a.g >= a.K ? 0 : b / blocks_per_group);
-        } else {
+                Unit<BITS> u[MT][2];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int k = b * kBlock + 32 * j;
-                if (k >= a.K) break;   // the same for every lane
-                uint32_t xb[NT][4];
-                tokens(j, xb);
-                if constexpr (MODE == kNarrow) {
-                    clear();
-                    products(j, xb, 0xffffffffu);
-                    fold(k / a.g);
-                } else {
-                    for (int sub = 0; sub < 32 / a.g; ++sub) {
-                        clear();
-                        products(j, xb, t * 8 / a.g == sub ? 0xffffffffu : 0u);
-                        fold(k / a.g + sub);
+                for (int m = 0; m < MT; ++m) units(m, j, u[m]);
+                for (int sub = 0; sub < 32 / a.g; ++sub) {
+                    const uint32_t mask = t * 8 / a.g == sub ? 0xffffffffu : 0u;
+                    float cs[NT][4];
+                    clear(cs);
+                    total(xb, mask, cs);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        float c[NT][4];
+                        clear(c);
+                        product(u[m], xb, mask, c);
+                        fold(m, 32 * j / a.g + sub, c, cs);
                     }
+                }
+            }
+        } else {
+            float c[MT][NT][4], cs[NT][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t xb[NT][4];
+                tokens(j, xb);
+                if (MODE == kNarrow || j == 0) {
+                    clear(cs);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) clear(c[m]);
+                }
+                total(xb, 0xffffffffu, cs);
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    Unit<BITS> u[2];
+                    units(m, j, u);
+                    product(u, xb, 0xffffffffu, c[m]);
+                    if (MODE == kNarrow ? 32 * j < left : j == 3) fold(m, MODE == kNarrow ? 32 * j / a.g : 0, c[m], cs);
                 }
             }
         }
+        __syncwarp();   // every lane has read the slot
+        if (s + depth < steps) {
+            if (lane == 0) {
+                load_weights(s + depth, slot);
+                load_tokens(s + depth, slot);
+            }
+            load_scales(b + depth * stride, slot);
+        }
+        cp_commit();
+        if (++slot == depth) {
+            slot = 0;
+            phase ^= 1u;
+        }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (!ok && lane == 0) {
+        // never leave with copies in flight (bounded): blocks `done` on, as far
+        // as they were issued
+        volatile int no_abort = 0;
+        for (int s = done; s < steps && s < done + depth; ++s)
+            if (!mbar_wait(&full[s % depth], (s / depth) & 1u, &no_abort)) break;
     }
 
     // ---- partial sums of the K slices: within the CTA, then the cluster
+    __syncthreads();   // the rings are free
+    float* red = reinterpret_cast<float*>(sm + S::kHead);   // [kWarps][kTok][kPitch]
 #pragma unroll
-    for (int m = 0; m < kTiles; ++m)
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int q = 0; q < NT; ++q)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                red[wk][8 * q + 2 * t + (i & 1)][(wr * kTiles + m) * 16 + g8 + 8 * (i >> 1)] = acc[m][q][i];
+            for (int i = 0; i < 4; ++i) {
+                const int col = 2 * t + (i & 1);   // its token, as above
+                red[(warp * kTok + 8 * q + ((col >> 1) | (col & 1) << 2)) * S::kPitch + m * 16 + g8 + 8 * (i >> 1)] =
+                    acc[m][q][i];
+            }
     __syncthreads();
     for (int e = threadIdx.x; e < kTok * kRows; e += kThreads) {
-        const int tok = e / kRows, r = e % kRows;
-        float v = red[0][tok][r];
+        const int tk = e / kRows, r = e % kRows;
+        if (tk >= a.n_tok) break;
+        float v = red[tk * S::kPitch + r];
 #pragma unroll
-        for (int w = 1; w < WK; ++w) v += red[w][tok][r];
-        red[0][tok][r] = v;   // each entry has one owner
+        for (int w = 1; w < kWarps; ++w) v += red[(w * kTok + tk) * S::kPitch + r];
+        red[tk * S::kPitch + r] = v;   // each entry has one owner
     }
     cg::cluster_group cluster = cg::this_cluster();
     if (ranks > 1) cluster.sync(); else __syncthreads();
-    constexpr int kOut = GATED ? 16 * WR : kRows;
-    for (int e = rank * kThreads + threadIdx.x; e < kTok * kOut; e += ranks * kThreads) {
-        const int tok = e / kOut, o = e % kOut, n = n0 + o;
-        if (tok >= a.n_tok || n >= a.N) continue;
-        // gated: o = 16 wr + r lies in tile (wr, 0), its partner in tile (wr, 1)
-        const int r = GATED ? (o >> 4) * 32 + (o & 15) : o;
+    for (int e = rank * kThreads + threadIdx.x; e < a.n_tok * kOut; e += ranks * kThreads) {
+        const int tk = e / kOut, r = e % kOut, n = n0 + r;
+        if (n >= a.N) continue;
         float v = 0.f, u = 0.f;
         for (int k = 0; k < ranks; ++k) {
-            const float* p = ranks > 1 ? cluster.map_shared_rank(&red[0][tok][r], k) : &red[0][tok][r];
+            float* p = red + tk * S::kPitch + r;
+            if (ranks > 1) p = cluster.map_shared_rank(p, k);
             v += p[0];
-            if constexpr (GATED) u += p[16];
+            if constexpr (GATED) u += p[kOut];
         }
+        v *= kScaleBack;
         float y;
         if constexpr (GATED) {
-            y = activate(v, a.act) * u;
+            y = activate(v, a.act) * (u * kScaleBack);
         } else {
             if (a.bias != nullptr) v += a.bias[n];
             y = activate(v, a.act);
-            if (a.residual != nullptr)
-                y += bf16_to_float(a.residual[tok * a.ldr + n]);
+            if (a.residual != nullptr) y += bf16_to_float(a.residual[tk * a.ldr + n]);
         }
-        a.Y[tok * a.ldy + n] = f32_to_bf16_bits(y);
+        a.Y[tk * a.ldy + n] = f32_to_bf16_bits(y);
     }
     if (ranks > 1) cluster.sync();   // no CTA leaves while its sums are read
+    if (threadIdx.x == 0 && *abort) report(a.status, GPTQ_ERR_TIMEOUT);
 }
 
 // Xq[t][k] = X[t][perm[k]] (perm entries outside [0, K) read as k), 8 values
@@ -419,19 +543,57 @@ __global__ void __launch_bounds__(256) gather_rows_kernel(const uint16_t* __rest
     }
 }
 
-template <int BITS, int MODE, int NT, bool GATED, int WR>
-cudaError_t launch_one(const Args& a, bool pdl, cudaStream_t stream) {
-    const int per = (GATED ? 16 : 32) * WR;
-    const int tiles = (a.N + per - 1) / per;
+// What a launch needs beside Args: the tokens' buffer and the code width.
+struct Launch {
+    const uint16_t* X;
+    int64_t ldx;
+    cudaStream_t stream;
+};
+
+template <int BITS, int MODE, int NT, int MT, bool GATED>
+cudaError_t launch_one(Args a, const Launch& l) {
+    using S = Shape<BITS, NT, MT>;
+    auto kern = decode_kernel<BITS, MODE, NT, MT, GATED>;
+    constexpr int kOut = GATED ? S::kRows / 2 : S::kRows;
+    const int tiles = (a.N + kOut - 1) / kOut;
     const int nblk = (a.K + kBlock - 1) / kBlock;
-    // split K over a cluster while there are fewer than two CTAs per SM and a
-    // warp keeps at least two blocks
+    // split K over a cluster while all CTAs still run in one wave (two per SM) and
+    // every warp keeps at least two blocks
     int ranks = 1;
-    while (ranks < 8 && tiles * ranks < 2 * num_sms() && nblk >= 4 * ranks * (kWarps / WR)) ranks *= 2;
+    while (ranks < 8 && 2 * tiles * ranks <= 2 * num_sms() && nblk >= 4 * ranks * kWarps) ranks *= 2;
+    const int steps = (nblk + kWarps * ranks - 1) / (kWarps * ranks);
+    const int ngb = MODE == kWide ? 1 : kBlock / a.g;
+    for (a.ngb_log2 = 0; (1 << a.ngb_log2) < ngb; ++a.ngb_log2) {}
+    const uint64_t bpg = a.g >= a.K ? nblk : a.g / kBlock;   // (kWide only)
+    a.blocks_per_group = static_cast<int>(bpg);
+    // magic = ceil(2^32 / bpg) overshoots by e / bpg with e < bpg: exact below
+    // block nblk if nblk e < 2^32 (a block's number itself where bpg is 1)
+    const uint64_t magic = bpg > 1 ? ((uint64_t{1} << 32) + bpg - 1) / bpg : 0;
+    a.group_magic = bpg > 1 && nblk * (magic * bpg - (uint64_t{1} << 32)) < (uint64_t{1} << 32)
+                        ? static_cast<uint32_t>(magic) : 0;
+    a.slot_bytes = (S::kWBytes + a.n_tok * 256 + 1023) / 1024 * 1024;
+    const int per = kWarps * (a.slot_bytes + S::kRows * 8 * ngb);
+    int room = ((NT * MT >= 8 ? kSmemOne : kSmemTwo) - S::kHead) / per;
+    if (room < 2) room = (kSmemOne - S::kHead) / per;
+    a.depth = room < 1 ? 1 : room > kMaxDepth ? kMaxDepth : room;
+    if (a.depth > steps) a.depth = steps;
+    const int smem = S::kHead + (a.depth * per > S::kRedBytes ? a.depth * per : S::kRedBytes);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    constexpr Swz kSwz = BITS == 8 ? Swz::k128 : BITS == 4 ? Swz::k64 : BITS == 2 ? Swz::k32 : Swz::kNone;
+    const uint64_t words = static_cast<uint64_t>(a.K) * BITS / 32;
+    CUtensorMap tw[2], tx;
+    // the packed words move as raw 32-bit elements (the map's fp32 type only sizes them)
+    for (int m = 0; m < (GATED ? 2 : 1); ++m)
+        if (!make_tmap_2d(&tw[m], false, a.mat[m].packed, words, a.N, words, 4 * BITS, kOut, kSwz))
+            return cudaErrorInvalidValue;
+    if (!GATED) tw[1] = tw[0];
+    if (!make_tmap_2d(&tx, true, l.X, a.K, a.n_tok, l.ldx, 64, a.n_tok, Swz::k128)) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(tiles, ranks);
     cfg.blockDim = dim3(kThreads);
-    cfg.stream = stream;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = l.stream;
     cudaLaunchAttribute attr[2];
     int n = 0;
     if (ranks > 1) {
@@ -439,37 +601,45 @@ cudaError_t launch_one(const Args& a, bool pdl, cudaStream_t stream) {
         attr[n].val.clusterDim = {1, static_cast<unsigned>(ranks), 1};
         ++n;
     }
-    if (pdl) {
+    if (a.gathered) {
         attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[n].val.programmaticStreamSerializationAllowed = 1;
         ++n;
     }
     cfg.attrs = attr;
     cfg.numAttrs = n;
-    return cudaLaunchKernelEx(&cfg, decode_kernel<BITS, MODE, NT, GATED, WR>, a);
+    return cudaLaunchKernelEx(&cfg, kern, tw[0], tw[1], tx, a);
 }
 
 template <int BITS, int MODE, bool GATED>
-cudaError_t launch_tokens(const Args& a, bool pdl, cudaStream_t stream) {
-    if (a.n_tok <= 8) return launch_one<BITS, MODE, 1, GATED, 1>(a, pdl, stream);
-    if (a.n_tok <= 16) return launch_one<BITS, MODE, 2, GATED, 2>(a, pdl, stream);
-    return launch_one<BITS, MODE, 4, GATED, 4>(a, pdl, stream);
+cudaError_t launch_tokens(const Args& a, const Launch& l) {
+    // Eight tokens: 64 weight rows per CTA from 4096 rows on (the tokens' work and
+    // a block's fixed work are shared by twice the weights: 8192 x 4096 at one
+    // token 8.4 against 11.9 us with 32 rows), fewer where 32 rows are needed to
+    // fill the GPU.
+    constexpr int kMany = MODE == kTiny ? 2 : 4;
+    if (a.n_tok <= 8 && (GATED ? 2 : 1) * static_cast<int64_t>(a.N) >= 4096)
+        return launch_one<BITS, MODE, 1, kMany, GATED>(a, l);
+    if (a.n_tok <= 8) return launch_one<BITS, MODE, 1, 2, GATED>(a, l);
+    if (a.n_tok <= 16) return launch_one<BITS, MODE, 2, 2, GATED>(a, l);
+    // (wide codes or tiny groups: 64 rows would not leave room for two blocks)
+    return launch_one<BITS, MODE, 4, MODE == kTiny || BITS == 8 ? 2 : 4, GATED>(a, l);
 }
 
 template <int BITS, bool GATED>
-cudaError_t launch_mode(const Args& a, bool pdl, cudaStream_t stream) {
-    if (a.g >= a.K || a.g % kBlock == 0) return launch_tokens<BITS, kWide, GATED>(a, pdl, stream);
-    if (a.g >= 32) return launch_tokens<BITS, kNarrow, GATED>(a, pdl, stream);
-    return launch_tokens<BITS, kTiny, GATED>(a, pdl, stream);
+cudaError_t launch_mode(const Args& a, const Launch& l) {
+    if (a.g >= a.K || a.g % kBlock == 0) return launch_tokens<BITS, kWide, GATED>(a, l);
+    if (a.g >= 32) return launch_tokens<BITS, kNarrow, GATED>(a, l);
+    return launch_tokens<BITS, kTiny, GATED>(a, l);
 }
 
 template <bool GATED>
-cudaError_t launch_bits(const Args& a, int bits, bool pdl, cudaStream_t stream) {
+cudaError_t launch_bits(const Args& a, int bits, const Launch& l) {
     switch (bits) {
-        case 2: return launch_mode<2, GATED>(a, pdl, stream);
-        case 3: return launch_mode<3, GATED>(a, pdl, stream);
-        case 4: return launch_mode<4, GATED>(a, pdl, stream);
-        default: return launch_mode<8, GATED>(a, pdl, stream);
+        case 2: return launch_mode<2, GATED>(a, l);
+        case 3: return launch_mode<3, GATED>(a, l);
+        case 4: return launch_mode<4, GATED>(a, l);
+        default: return launch_mode<8, GATED>(a, l);
     }
 }
 
@@ -489,7 +659,7 @@ gptq_status launch_linear_decode(const LinearCall& c, cudaStream_t stream) {
     a.K = static_cast<int>(c.d_col);
     a.N = static_cast<int>(c.d_row);
     a.g = (c.group == -1 || c.group > a.K) ? a.K : c.group;
-    a.words = c.d_col * c.bits / 32;
+    a.status = c.status;
     a.bias = c.bias;
     a.ldr = c.ldr;
     a.ldy = c.ldy;
@@ -497,22 +667,21 @@ gptq_status launch_linear_decode(const LinearCall& c, cudaStream_t stream) {
     int64_t launches = 0;
     for (int64_t t0 = 0; t0 < c.n_tok; t0 += kMaxTok) {
         a.n_tok = static_cast<int>(c.n_tok - t0 < kMaxTok ? c.n_tok - t0 : kMaxTok);
-        a.X = c.X + t0 * c.ldx;
-        a.ldx = c.ldx;
+        Launch l = {c.X + t0 * c.ldx, c.ldx, stream};
         if (gather) {
             uint16_t* xq = static_cast<uint16_t*>(c.ws);
             const int64_t work = (static_cast<int64_t>(a.n_tok) * (a.K / 8) + 255) / 256;
             const int blocks = static_cast<int>(work < 8 * num_sms() ? work : 8 * num_sms());
-            gather_rows_kernel<<<blocks, 256, 0, stream>>>(a.X, a.ldx, a.n_tok, a.K, c.perm, xq);
+            gather_rows_kernel<<<blocks, 256, 0, stream>>>(l.X, l.ldx, a.n_tok, a.K, c.perm, xq);
             if (cudaGetLastError() != cudaSuccess) return GPTQ_ERR_CUDA;
-            a.X = xq;
-            a.ldx = c.d_col;
+            l.X = xq;
+            l.ldx = c.d_col;
             ++launches;
         }
         a.residual = c.residual == nullptr ? nullptr : c.residual + t0 * c.ldr;
         a.Y = c.Y + t0 * c.ldy;
-        const cudaError_t e = gated ? launch_bits<true>(a, c.bits, gather, stream)
-                                    : launch_bits<false>(a, c.bits, gather, stream);
+        a.gathered = gather;
+        const cudaError_t e = gated ? launch_bits<true>(a, c.bits, l) : launch_bits<false>(a, c.bits, l);
         if (e != cudaSuccess) return GPTQ_ERR_CUDA;
         ++launches;
     }

@@ -41,6 +41,8 @@ bool make_tmap_2d(CUtensorMap* map, bool bf16, const void* base, uint64_t inner,
     return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
                const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                swizzle == Swz::k128 ? CU_TENSOR_MAP_SWIZZLE_128B
+               : swizzle == Swz::k64      ? CU_TENSOR_MAP_SWIZZLE_64B
+               : swizzle == Swz::k32      ? CU_TENSOR_MAP_SWIZZLE_32B
                : swizzle == Swz::k128Atom32 ? CU_TENSOR_MAP_SWIZZLE_128B_ATOM_32B
                                             : CU_TENSOR_MAP_SWIZZLE_NONE,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;

@@ -43,13 +43,12 @@ class Layer:
             return oracle.bf16_round((s * m.astype(np.float32)).astype(np.float32)).astype(np.float64)
         return s.astype(np.float64) * m
 
-    def offsets(self):
-        """s (c + q) and s (c + z), the magnitudes that the decode form's
-        per-group sums pass through (c = 128, 2176 at 8 bits), float64."""
-        c = 2176.0 if self.bits == 8 else 128.0
+    def magnitudes(self):
+        """s (q + |z|), the magnitudes that the decode form's per-group sums
+        (of x q and of z x) pass through, float64."""
         gi = np.arange(self.d_col) // self.gg
         s = self.scales[gi, :].T.astype(np.float64)
-        return s * (2 * c + self.codes().astype(np.float64) + np.abs(self.zeros[gi, :].T))
+        return s * (self.codes().astype(np.float64) + np.abs(self.zeros[gi, :].T))
 
     def cuda(self):
         return (torch.from_numpy(self.packed.view(np.int32)).cuda(), torch.from_numpy(self.scales).cuda(),
@@ -108,7 +107,7 @@ def product(X, layer, perm, form):
 
     decode: per 16 codes one tensor-core step, whose rounding is at most one
     unit of 2^-23 of the running magnitude, which stays below
-    sum_k |x_k| s (2c + q + |z|); per group three more roundings, per 128-code
+    sum_k |x_k| s (q + |z|); per group three more roundings, per 128-code
     block one, plus the joins: K / 16 + 3 K / 8 (groups of 8) + 64 of them
     cover every group size.
     many: at most one rounding per 16 terms plus the sums inside a step, each
@@ -119,7 +118,7 @@ def product(X, layer, perm, form):
     w = layer.weights(form != "decode")
     y = x @ w.T
     if form == "decode":
-        bound = (K / 16 + 3 * K / min(128, layer.gg) + 64) * EPS32 * (np.abs(x) @ layer.offsets().T)
+        bound = (K / 16 + 3 * K / min(128, layer.gg) + 64) * EPS32 * (np.abs(x) @ layer.magnitudes().T)
     else:
         bound = 2 * (K / 16 + 64) * EPS32 * (np.abs(x) @ np.abs(w).T)
     return y, bound

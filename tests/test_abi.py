@@ -316,9 +316,9 @@ _LAYERS = ("pk", "sc", "ze", "pk2", "sc2", "ze2")
 _EPILOGUE = {
     # name: argument order (argument: type by its name in _TYPES)
     "gptq_dequant_matmul_linear": ("X", "n", "k", "ldx", *_LAYER, "perm", "r", "bits", "g", "bias", "act", "res",
-                                   "ldr", "Y", "ldy", "ws", "wsb", "stream"),
-    "gptq_dequant_matmul_gated": ("X", "n", "k", "ldx", *_LAYERS, "perm", "r", "bits", "g", "act", "Y", "ldy", "ws",
-                                  "wsb", "stream"),
+                                   "ldr", "Y", "ldy", "st", "ws", "wsb", "stream"),
+    "gptq_dequant_matmul_gated": ("X", "n", "k", "ldx", *_LAYERS, "perm", "r", "bits", "g", "act", "Y", "ldy", "st",
+                                  "ws", "wsb", "stream"),
     "gptq_dequant_gemm_linear": ("X", "n", "k", "ldx", *_LAYER, "perm", "r", "bits", "g", "bias", "act", "res", "ldr",
                                  "pre", "ldpre", "Y", "ldy", "st", "ws", "wsb", "stream"),
     "gptq_dequant_gemm_gated": ("X", "n", "k", "ldx", *_LAYERS, "perm", "r", "bits", "g", "act", "gate", "ldgate",
@@ -382,7 +382,7 @@ def test_products_with_an_epilogue_refuse_on_the_host(pkg, name):
     for a in ("pk", "pk2"):
         if a in order:
             assert call(**{a: _odd(8)}) == 1               # packed rows by 16-byte units
-    for a in ("sc", "ze", "sc2", "ze2", "perm", "bias", "dbias"):
+    for a in ("sc", "ze", "sc2", "ze2", "perm", "bias", "dbias", "st"):
         if a in order:
             assert call(**{a: _odd(2)}) == 1, a
     for a in ("X", "Y", "res", "dX", "gate", "up", "dGate", "dUp", "dPre"):

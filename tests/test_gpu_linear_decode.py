@@ -59,9 +59,10 @@ def test_linear_matches_float64(n, d_col, d_row, bits, g, with_perm, activation,
     want, bound, _, _ = lt.linear(X, layer, perm, "decode", bias, activation, res)
     buf, Y = lt.blank(n, d_row)
     ws = torch.full((q.gptq_dequant_matmul_linear_workspace_size(n, d_col),), 255, dtype=torch.uint8, device="cuda")
-    q.gptq_dequant_matmul_linear(X.cuda(), *layer.cuda(), None if perm is None else torch.from_numpy(perm).cuda(),
-                                 bits, g, Y, ws, bias=None if bias is None else torch.from_numpy(bias).cuda(),
-                                 activation=activation, residual=None if res is None else res.cuda())
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q.gptq_dequant_matmul_linear(X.cuda(), *layer.cuda(), lt.cuda(perm), bits, g, Y, ws, bias=lt.cuda(bias),
+                                 activation=activation, residual=lt.cuda(res), dev_status=st)
+    assert q.gptq_sync_status(st) == 0
     lt.check(Y, want, bound, "Y")
     lt.untouched(buf, d_row)
 
