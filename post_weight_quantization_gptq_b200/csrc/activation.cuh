@@ -2,7 +2,10 @@
 // (gptq_activation in the header).  Each is written so that no intermediate
 // value overflows into a NaN for a finite x, and so that the small values left
 // of zero keep their relative accuracy (erfc and 1 / (1 + exp) instead of
-// 1 + erf and 1 + tanh).
+// 1 + erf and 1 + tanh).  exp and the quotient are CUDA's approximate forms: a
+// few units of 2^-23 plus the rounding of exp's argument, against 2^-8 of the
+// bf16 outputs (with the exact forms a 256 x 256 output tile spent 56 us in its
+// GELU, almost half of what its product takes).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -16,13 +19,17 @@ constexpr float kInvSqrt2 = 0.70710678118654752440f;
 constexpr float kInvSqrt2Pi = 0.39894228040143267794f;
 constexpr float kGeluCubic = 0.044715f;
 
-// exp(-x) overflows to +inf for x < -88: the quotient is then -0
-__device__ __forceinline__ float sigmoid_f(float x) { return 1.f / (1.f + expf(-x)); }
+// 1 / (1 + exp(-x)); exp(-x) overflows to +inf for x < -88: 0 then
+__device__ __forceinline__ float sigmoid_f(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-x)));
+    return r;
+}
 
 // (1 + tanh(u)) / 2 = 1 / (1 + exp(-2u)), u = sqrt(2/pi) (x + 0.044715 x^3)
 __device__ __forceinline__ float gelu_tanh_half(float x) {
     const float u = kSqrt2OverPi * (x + kGeluCubic * x * x * x);
-    return 1.f / (1.f + expf(-2.f * u));
+    return sigmoid_f(2.f * u);
 }
 
 __device__ __forceinline__ float activate(float x, int act) {
@@ -39,7 +46,7 @@ __device__ __forceinline__ float activate_slope(float x, int act) {
     switch (act) {
         case GPTQ_ACT_RELU: return x > 0.f ? 1.f : 0.f;
         case GPTQ_ACT_GELU:
-            return 0.5f * erfcf(-x * kInvSqrt2) + x * kInvSqrt2Pi * expf(-0.5f * x * x);
+            return 0.5f * erfcf(-x * kInvSqrt2) + x * kInvSqrt2Pi * __expf(-0.5f * x * x);
         case GPTQ_ACT_GELU_TANH: {
             const float h = gelu_tanh_half(x), p = h * (1.f - h);
             // p is 0 where x^2 may overflow

@@ -111,6 +111,24 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
     return mbar_wait_ns(bar, parity, abort, kWaitLimitNs);
 }
 
+// The same for waits that are usually short: the clock is first read after some
+// failed tries (reading it costs more than such a wait takes).
+__device__ __forceinline__ bool mbar_wait_short(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    uint64_t t0 = 0;
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 255u) == 0u) {
+            if (*abort) return false;
+            const uint64_t now = globaltimer();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > kWaitLimitNs) {
+                *abort = 1;
+                return false;
+            }
+        }
+    }
+}
+
 // Timeout probe (a test of the expiry path, armed from the host through
 // gptq_debug_arm_wait_probe): when probe_ns > 0 the kernel's MMA-issuing
 // thread first waits, bounded by probe_ns, on a barrier that nothing ever

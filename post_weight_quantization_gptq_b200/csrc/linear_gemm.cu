@@ -11,11 +11,14 @@
 // 128 x 256 accumulators, all of tensor memory) and sweeps the contraction in
 // stages of 64:
 //   warp 0      TMA: the stage's tokens (2 x 128 x 64 bf16, 128-byte swizzle)
-//   warp 10     TMA: the stage's packed words, in a ring of their own
+//   warp 2      TMA: the stage's packed words, in a ring of their own
 //   warp 1      tensor memory and the MMAs (kind::f16, M 128, N 256, K 16)
-//   warps 2..9  dequantize the stage's 256 x 64 weights into a bf16 tile in
-//               shared memory, one thread per 64 codes of one weight row; after
-//               the sweep they drain the accumulators through the epilogue
+//   warps 3..18 dequantize the stage's 256 x 64 weights into a bf16 tile in
+//               shared memory, one thread per 64 codes of one weight row; two
+//               groups of eight warps take every other stage, so that one
+//               group's hand-over (waits, fence, arrivals: 0.35 us) hides behind
+//               the other's arithmetic.  After the sweep they drain the
+//               accumulators through the epilogue
 // linear    the tile's columns are 256 weight rows n, the stage 64 of their k:
 //           the weight tile is K-major.
 // gated     the columns are 128 rows of the gate and the same 128 of the up
@@ -25,12 +28,9 @@
 //           writes 64 codes of one row as 128 bytes, which now is the MN-major
 //           layout of the same tile; the two matrices of the gated form are two
 //           sweeps into one accumulator.
-// A thread looks its weights up: the 2^bits weights of a group are computed
-// once (8 instructions per 4 of them), kept as bytes in registers and picked
-// by byte permutes, 3 instructions per 4-bit code, so that 16,384 codes per
-// stage take about half of the 1024 cycles of the stage's MMAs; 8-bit codes are
-// computed one by one.  A tile whose second 128 tokens lie past the end skips
-// that half's loads and MMAs.
+// Dequantization is arithmetic on two pipes (see weights8), about half of the
+// stage's 1024 MMA cycles.  A tile whose second 128 tokens lie past the end
+// skips that half's loads and MMAs.
 //
 // Tiles that do not fill the last wave of SMs split the contraction: their
 // partial tiles go to the workspace and a second kernel adds them in order and
@@ -56,7 +56,8 @@ constexpr int kHalfBytes = 128 * BK * 2;      // 16 KB: one half's tokens
 constexpr int kABytes = 2 * kHalfBytes;
 constexpr int kBBytes = TN * BK * 2;          // 32 KB: one dequantized tile
 constexpr int kMaxBBufs = 3, kMaxPStages = 6;
-constexpr int kThreads = 352;
+constexpr int kDeqWarps = 16;                 // two groups of 8, each every other stage
+constexpr int kThreads = 32 * (3 + kDeqWarps);
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSms = 148;                     // SMs of the device this library is built for
 constexpr int kMinStages = 8;                 // least stages of a split tile's part
@@ -185,83 +186,77 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[2 * B
     }
 }
 
-// The 2^BITS weights of a group, bf16(s (q - z)), as byte tables: entry 4j + i
-// has its low byte in byte i of lo[j] and its high byte in byte i of hi[j].
+// A group's parameters as the arithmetic below takes them.  A code at bits
+// BITS p .. of a word (p = 0 .. 3) is masked there and ORed with the exponent of
+// 2^23: the float 2^23 + q 2^(BITS p), no shift.  Less 2^23 + z 2^(BITS p) that
+// is (q - z) 2^(BITS p) exactly, and times s 2^-(BITS p) it is the fp32 product
+// s (q - z), rounded once.  8-bit codes are put at bit 0 by a byte permute.
 template <int BITS>
-struct Table {
-    static constexpr int W = (1 << BITS) / 4;
-    uint32_t lo[W], hi[W];
+struct Group {
+    static constexpr int kPairs = BITS == 8 ? 1 : 2;
+    uint64_t off[kPairs], scale[kPairs];   // positions (0, 1) and (2, 3)
+    __device__ __forceinline__ void set(float s, float z) {
+        constexpr float kBase = 8388608.f;
+        if constexpr (BITS == 8) {
+            off[0] = pk2(kBase + z, kBase + z);
+            scale[0] = pk2(s, s);
+        } else {
+            constexpr float k1 = 1 << BITS, k2 = 1 << (2 * BITS), k3 = 1 << (3 * BITS);
+            off[0] = pk2(kBase + z, fmaf(z, k1, kBase));
+            off[1] = pk2(fmaf(z, k2, kBase), fmaf(z, k3, kBase));
+            scale[0] = pk2(s, s * (1.f / k1));
+            scale[1] = pk2(s * (1.f / k2), s * (1.f / k3));
+        }
+    }
 };
-template <int BITS>
-__device__ __forceinline__ void build_table(float s, float z, Table<BITS>& tab) {
-    const uint64_t s2 = pk2(s, s), z2 = pk2(z, z);
-#pragma unroll
-    for (int j = 0; j < Table<BITS>::W; ++j) {
-        uint32_t r[2];
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            const float q0 = static_cast<float>(4 * j + 2 * p);
-            const uint64_t v = mul2(sub2(pk2(q0, q0 + 1.f), z2), s2);  // q - z exact, one rounding
-            float lo, hi;
-            asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-            r[p] = f32x2_to_bf16x2(lo, hi);
-        }
-        tab.lo[j] = __byte_perm(r[0], r[1], 0x6420);
-        tab.hi[j] = __byte_perm(r[0], r[1], 0x7531);
-    }
-}
 
-// Codes 8c .. 8c+7 of the words as four bf16x2 weights.  Two and three bits: the
-// codes spread to one per nibble select among the table's bytes directly.
+// Codes 8c .. 8c+7 of a thread's 64 as four bf16x2 weights: per 8 codes 8 masks
+// and a shift, 4 packings and 8 packed fp32 operations on the other pipe (a
+// table look-up by byte permutes takes 23 on the first, which runs 64 lanes per
+// cycle and bound the sweep).
 template <int BITS>
-__device__ __forceinline__ void lookup(const uint32_t (&w)[2 * BITS], int c, const Table<BITS>& tab,
-                                       uint32_t (&o)[4]) {
-    if constexpr (BITS == 4) {
-        lookup8(w[c], tab.lo, tab.hi, o);
+__device__ __forceinline__ void weights8(const uint32_t (&w)[2 * BITS], int c, const Group<BITS>& g, uint32_t (&o)[4]) {
+    constexpr uint32_t kMagic = 0x4B000000u;
+    uint64_t f[4];
+    if constexpr (BITS == 8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t x = w[2 * c + (i >> 1)];
+            const int b = 2 * (i & 1);
+            f[i] = pk2(__uint_as_float(__byte_perm(x, kMagic, 0x7440 + b)), __uint_as_float(__byte_perm(x, kMagic, 0x7441 + b)));
+        }
     } else {
-        uint32_t sel;
-        if constexpr (BITS == 3) {
+        uint32_t v;   // the 8 codes from bit 0 on
+        if constexpr (BITS == 4) {
+            v = w[c];
+        } else if constexpr (BITS == 2) {
+            v = (c & 1) ? w[c >> 1] >> 16 : w[c >> 1];
+        } else {
             const int b = (24 * c) >> 5, sh = (24 * c) & 31;
-            const uint32_t v = sh <= 8 ? (w[b] >> sh) : __funnelshift_r(w[b], w[b + 1 < 6 ? b + 1 : 5], sh);
-            const uint32_t u = (v & 0xFFFu) | ((v & 0xFFF000u) << 4);   // codes 0..3 | 4..7
-            sel = (u & 0x00070007u) | ((u << 1) & 0x00700070u) | ((u << 2) & 0x07000700u) |
-                  ((u << 3) & 0x70007000u);
-        } else {
-            uint32_t v = __byte_perm(w[c >> 1], 0, (c & 1) ? 0x4342 : 0x4140);  // codes 0..3 | 4..7
-            v = (v | (v << 4)) & 0x0F0F0F0Fu;
-            sel = (v | (v << 2)) & 0x33333333u;
+            v = sh <= 8 ? (w[b] >> sh) : __funnelshift_r(w[b], w[b + 1 < 6 ? b + 1 : 5], sh);
         }
-        const uint32_t l1 = BITS == 3 ? tab.lo[Table<BITS>::W - 1] : 0, h1 = BITS == 3 ? tab.hi[Table<BITS>::W - 1] : 0;
+        const uint32_t u = v >> (4 * BITS);
+        constexpr uint32_t kMask = (1u << BITS) - 1u;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t s4 = (sel >> (16 * h)) & 0xFFFFu;
-            const uint32_t L = prmt(tab.lo[0], l1, s4), H = prmt(tab.hi[0], h1, s4);
-            o[2 * h] = __byte_perm(L, H, 0x5140);
-            o[2 * h + 1] = __byte_perm(L, H, 0x7362);
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t x = i < 2 ? v : u;
+            const int at = 2 * BITS * (i & 1);
+            f[i] = pk2(__uint_as_float((x & (kMask << at)) | kMagic),
+                       __uint_as_float((x & (kMask << (at + BITS))) | kMagic));
         }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint64_t r = mul2(sub2(f[i], g.off[i % Group<BITS>::kPairs]), g.scale[i % Group<BITS>::kPairs]);
+        float lo, hi;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(r));
+        o[i] = f32x2_to_bf16x2(lo, hi);
     }
 }
 
-// Eight 8-bit codes directly: 2^23 + q less 2^23 + z is q - z exactly.
-__device__ __forceinline__ void direct8(const uint32_t (&w)[16], int c, uint64_t s2, uint64_t off2,
-                                        uint32_t (&o)[4]) {
-    float f[8];
-    chunk_codes<8>(w, c, f);
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-        const uint64_t v = mul2(sub2(pk2(f[2 * p], f[2 * p + 1]), off2), s2);
-        if (p & 1) {   // the conversion pipe takes half, the fp32 pipe the other half
-            float lo, hi;
-            asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-            o[p] = f32x2_to_bf16x2(lo, hi);
-        } else {
-            o[p] = bf16x2_rne(v);
-        }
-    }
-}
-
-// GPS: groups per 64 codes (1 where g is a multiple of 64 or one group spans the row).
-template <int BITS, int GPS, int MODE>
+// GPT: groups in a thread's 64 codes (1 where g is a multiple of 64 or one group
+// spans the row).
+template <int BITS, int GPT, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     packed_gemm_kernel(const __grid_constant__ CUtensorMap tma0, const __grid_constant__ CUtensorMap tma1,
                        const __grid_constant__ CUtensorMap tmp0, const __grid_constant__ CUtensorMap tmp1,
@@ -295,10 +290,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int s = 0; s < G::kPStages; ++s) {
             mbar_init(&bars->pfull[s], 1);
-            mbar_init(&bars->pempty[s], 256);
+            mbar_init(&bars->pempty[s], G::kPairs ? kDeqWarps : kDeqWarps / 2);
         }
         for (int b = 0; b < G::kBBufs; ++b) {
-            mbar_init(&bars->bfull[b], 256);
+            mbar_init(&bars->bfull[b], kDeqWarps / 2);
             mbar_init(&bars->bempty[b], 1);
         }
         mbar_init(&bars->acc_full, 1);
@@ -323,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int i = 0;
             for (int it = k0; it < k1 && !*abort; ++it, ++i) {
                 const int st = i % kAStages;
-                if (!mbar_wait(&bars->aempty[st], ((i / kAStages) & 1u) ^ 1u, abort)) break;
+                if (!mbar_wait_short(&bars->aempty[st], ((i / kAStages) & 1u) ^ 1u, abort)) break;
                 const bool second = MODE == kBack && it >= a.nk1;
                 const CUtensorMap* map = second ? &tma1 : &tma0;
                 const int x = (second ? it - a.nk1 : it) * BK;
@@ -335,20 +330,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             volatile int no_abort = 0;
             for (int j = 0; j < min(i, kAStages); ++j) {
                 const int i2 = i - 1 - j;
-                if (!mbar_wait(&bars->afull[i2 % kAStages], (i2 / kAStages) & 1u, &no_abort)) {
+                if (!mbar_wait_short(&bars->afull[i2 % kAStages], (i2 / kAStages) & 1u, &no_abort)) {
                     *abort = 1;
                     break;
                 }
             }
         }
-    } else if (warp == 10) {
+    } else if (warp == 2) {
         // ------------------------------------------------ TMA: packed words
         if (lane == 0) {
             constexpr int kStep = G::kPairs ? 2 : 1;
             int i = 0;
             for (int it = k0; it < k1 && !*abort; it += kStep, ++i) {
                 const int ps = i % G::kPStages;
-                if (!mbar_wait(&bars->pempty[ps], ((i / G::kPStages) & 1u) ^ 1u, abort)) break;
+                if (!mbar_wait_short(&bars->pempty[ps], ((i / G::kPStages) & 1u) ^ 1u, abort)) break;
                 uint8_t* dst = pbuf + ps * G::kSlot;
                 mbar_arrive_expect_tx(&bars->pfull[ps], G::kSlot);
                 if constexpr (MODE == kBack) {
@@ -368,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             volatile int no_abort = 0;
             for (int j = 0; j < min(i, G::kPStages); ++j) {
                 const int i2 = i - 1 - j;
-                if (!mbar_wait(&bars->pfull[i2 % G::kPStages], (i2 / G::kPStages) & 1u, &no_abort)) {
+                if (!mbar_wait_short(&bars->pfull[i2 % G::kPStages], (i2 / G::kPStages) & 1u, &no_abort)) {
                     *abort = 1;
                     break;
                 }
@@ -381,8 +376,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (int i = 0; i < k1 - k0; ++i) {
                 const int st = i % kAStages, b = i % G::kBBufs;
-                if (!mbar_wait(&bars->afull[st], (i / kAStages) & 1u, abort) ||
-                    !mbar_wait(&bars->bfull[b], (i / G::kBBufs) & 1u, abort)) {
+                if (!mbar_wait_short(&bars->afull[st], (i / kAStages) & 1u, abort) ||
+                    !mbar_wait_short(&bars->bfull[b], (i / G::kBBufs) & 1u, abort)) {
                     ok = false;
                     break;
                 }
@@ -405,79 +400,72 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok) mma_commit(&bars->acc_full);
             mma_commit(&bars->drain);
             volatile int no_abort = 0;
-            if (!mbar_wait(&bars->drain, 0, &no_abort)) *abort = 1;
+            if (!mbar_wait_short(&bars->drain, 0, &no_abort)) *abort = 1;
         }
     } else {
         // ------------------------------------------------ dequantize
-        const int j = threadIdx.x - 64;   // 0..255: the thread's 128 bytes of the weight tile
+        const int j = (threadIdx.x - 96) & 255;   // the thread's 128 bytes of the weight tile
+        const int team = (threadIdx.x - 96) >> 8; // which stages it takes
         // forward: weight row `wrow` of matrix `mi`; backward: row 64 it + (j & 63),
         // columns n0 + 64 (j >> 6) on
         const int mi = MODE == kGated ? j >> 7 : 0;
         const int wrow = n0 + (MODE == kGated ? (j & 127) : j);
         const int kcol = n0 + 64 * (j >> 6);
         const int groups = (a.d_col + a.g - 1) / a.g;
-        float s[GPS] = {}, z[GPS] = {}, s_nx[GPS], z_nx[GPS];
-        auto pair = [&](const PackedMatrix& m, int gi, int row, bool in, float& sv, float& zv) {
-            sv = 0.f;   // rows and columns past the layer: weights 0
-            zv = 0.f;
-            if (in) {
-                const int64_t at = static_cast<int64_t>(gi) * a.d_row + row;
-                sv = __ldg(m.scales + at);
-                zv = static_cast<float>(__ldg(m.zeros + at));
-            }
-        };
-        // the scales of stage `it` (forward with GPS 1: of group `it`)
+        // this stage's scales and zero points, and the next one's: loaded a stage
+        // ahead and first touched then (even the conversion to float would wait)
+        float s[GPT] = {}, s_nx[GPT];
+        int z[GPT] = {}, z_nx[GPT];
+        const int span = GPT == 1 ? a.g / BK : 1;              // stages per group (forward)
+        int gi = GPT == 1 && MODE != kBack ? (k0 + team) / span : 0, rem = GPT == 1 && MODE != kBack ? (k0 + team) % span : 0;
+        const int back_group = GPT == 1 ? kcol / a.g : kcol / 64 * GPT;
         auto fetch = [&](int it) {
 #pragma unroll
-            for (int q = 0; q < GPS; ++q) {
+            for (int q = 0; q < GPT; ++q) {
+                int group, row, m;
+                bool in;
                 if constexpr (MODE == kBack) {
-                    const bool second = it >= a.nk1;
-                    const int row = (second ? it - a.nk1 : it) * BK + (j & 63);
-                    const int gi = GPS == 1 ? kcol / a.g : (kcol / 64) * GPS + q;
-                    pair(a.mat[second ? 1 : 0], gi, row, it < k1 && row < a.d_row && kcol < a.d_col, s_nx[q], z_nx[q]);
+                    m = it >= a.nk1 ? 1 : 0;
+                    row = (m ? it - a.nk1 : it) * BK + (j & 63);
+                    group = back_group + q;
+                    in = it < k1 && row < a.d_row && kcol < a.d_col;
                 } else {
-                    const int gi = it * GPS + q;
-                    pair(a.mat[mi], gi, wrow, wrow < a.d_row && gi < groups, s_nx[q], z_nx[q]);
+                    m = mi;
+                    row = wrow;
+                    group = GPT == 1 ? gi : it * GPT + q;
+                    in = it < k1 && row < a.d_row && group < groups;
+                }
+                s_nx[q] = 0.f;   // rows and columns past the layer: weights 0
+                z_nx[q] = 0;
+                if (in) {
+                    const int64_t at = static_cast<int64_t>(group) * a.d_row + row;
+                    s_nx[q] = __ldg(a.mat[m].scales + at);
+                    z_nx[q] = __ldg(a.mat[m].zeros + at);
                 }
             }
-        };
-        constexpr bool kByGroup = MODE != kBack && GPS == 1;   // parameters change only with the group
-        int cur_g = kByGroup ? k0 * BK / a.g : 0;
-        int next_start = k0 * BK;                              // kByGroup: where group cur_g takes over
-        fetch(kByGroup ? cur_g : k0);
-        constexpr bool kTable = BITS != 8;
-        Table<BITS == 8 ? 2 : BITS> tab;
-        uint64_t s2 = 0, off2 = 0;
-        auto set = [&](int q) {
-            if constexpr (kTable) {
-                build_table<BITS>(s[q], z[q], tab);
-            } else {
-                s2 = pk2(s[q], s[q]);
-                const float off = 8388608.f + z[q];
-                off2 = pk2(off, off);
+            if constexpr (GPT == 1 && MODE != kBack) {   // the group two stages on
+                rem += 2;
+                if (rem >= span) { rem -= span; ++gi; }
+                if (rem >= span) { rem -= span; ++gi; }
             }
         };
+        fetch(k0 + team);
+        Group<BITS> grp;
+        uint32_t dst_off[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) dst_off[c] = j * 128 + ((c ^ (j & 7)) << 4);
         bool ok = true;
-        for (int it = k0, i = 0; it < k1; ++it, ++i) {
+        for (int it = k0 + team, i = team; it < k1; it += 2, i += 2) {
             const int pi = G::kPairs ? i >> 1 : i;
             const int ps = pi % G::kPStages, b = i % G::kBBufs;
-            if (kByGroup ? it * BK >= next_start : true) {
 #pragma unroll
-                for (int q = 0; q < GPS; ++q) {
-                    s[q] = s_nx[q];
-                    z[q] = z_nx[q];
-                }
-                if constexpr (kByGroup) {
-                    ++cur_g;
-                    next_start = cur_g * a.g;
-                    fetch(cur_g);
-                } else {
-                    fetch(it + 1);
-                }
-                if constexpr (GPS == 1) set(0);
+            for (int q = 0; q < GPT; ++q) {
+                s[q] = s_nx[q];
+                z[q] = z_nx[q];
             }
-            if (!mbar_wait(&bars->pfull[ps], (pi / G::kPStages) & 1u, abort) ||
-                !mbar_wait(&bars->bempty[b], ((i / G::kBBufs) & 1u) ^ 1u, abort)) {
+            fetch(it + 2);
+            if constexpr (GPT == 1) grp.set(s[0], static_cast<float>(z[0]));
+            if (!mbar_wait_short(&bars->pfull[ps], (pi / G::kPStages) & 1u, abort)) {
                 ok = false;
                 break;
             }
@@ -491,30 +479,37 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             uint32_t w[2 * BITS];
             load_words<BITS>(src, w);
-            const uint32_t row = smem_u32(bbuf + b * kBBytes) + j * 128;
+            if (!mbar_wait_short(&bars->bempty[b], ((i / G::kBBufs) & 1u) ^ 1u, abort)) {
+                ok = false;
+                break;
+            }
+            const uint32_t tile_at = smem_u32(bbuf + b * kBBytes);
 #pragma unroll
-            for (int c = 0; c < BK / 8; ++c) {
-                if constexpr (GPS > 1) {
-                    if (c % (8 / GPS) == 0) set(c / (8 / GPS));
+            for (int c = 0; c < 8; ++c) {
+                if constexpr (GPT > 1) {
+                    if (c % (8 / GPT) == 0) grp.set(s[c / (8 / GPT)], static_cast<float>(z[c / (8 / GPT)]));
                 }
                 uint32_t o[4];
-                if constexpr (kTable) lookup<BITS>(w, c, tab, o);
-                else direct8(w, c, s2, off2, o);
-                sts128_u(row + ((c ^ (j & 7)) << 4), make_uint4(o[0], o[1], o[2], o[3]));
+                weights8<BITS>(w, c, grp, o);
+                sts128_u(tile_at + dst_off[c], make_uint4(o[0], o[1], o[2], o[3]));
             }
             fence_async_smem();
-            mbar_arrive(&bars->bfull[b]);
-            // the slot's words have been used (their loads completed) before it may be refilled
-            if (!G::kPairs || (i & 1) || it + 1 == k1) mbar_arrive(&bars->pempty[ps]);
+            // one arrival per warp (arrivals on a barrier are serialized)
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&bars->bfull[b]);
+                // the slot's words have been used (their loads completed) before it may be refilled
+                mbar_arrive(&bars->pempty[ps]);
+            }
         }
         // ------------------------------------------------ drain: tensor memory -> output
-        if (ok && mbar_wait(&bars->acc_full, 0, abort)) {
+        if (ok && mbar_wait_short(&bars->acc_full, 0, abort)) {
             tc_fence_after();
             const int q = warp & 3;           // tensor-memory lane quarter of this warp
-            const int side = (warp - 2) >> 2; // it shares the quarter's chunks with one other warp
+            const int side = (warp - 3) >> 2; // it shares the quarter's chunks with three other warps
             const int chunks = MODE == kGated && slot < 0 ? TN / 64 : TN / 32;
 #pragma unroll 1
-            for (int e = side; e < halves * chunks; e += 2) {
+            for (int e = side; e < halves * chunks; e += kDeqWarps / 4) {
                 const int h = e / chunks, c = e % chunks;
                 const int t = t0 + h * 128 + 32 * q + lane;
                 const uint32_t at = tmem + (static_cast<uint32_t>(32 * q) << 16) + h * TN + c * 32;
@@ -618,10 +613,10 @@ Plan make_plan(int64_t n_tok, int64_t N, int nk, bool gated, bool pairs) {
     return p;
 }
 
-template <int BITS, int GPS, int MODE>
+template <int BITS, int GPT, int MODE>
 cudaError_t launch_one(const CUtensorMap (&ta)[2], const CUtensorMap (&tp)[2], const Args& a, int units,
                        cudaStream_t stream) {
-    auto kern = packed_gemm_kernel<BITS, GPS, MODE>;
+    auto kern = packed_gemm_kernel<BITS, GPT, MODE>;
     constexpr int kSmem = Geom<BITS, MODE>::kSmem;
     static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
