@@ -7,10 +7,10 @@
 // products of two bf16 values are exact, sums are fp32, outputs are rounded to
 // bf16 once.
 //
-// One kernel for the three.  A CTA owns a tile of 256 tokens x 256 columns (two
-// 128 x 256 accumulators, all of tensor memory) and sweeps the contraction in
-// stages of 64:
-//   warp 0      TMA: the stage's tokens (2 x 128 x 64 bf16, 128-byte swizzle)
+// One kernel for the three, in two sizes: a CTA with a tile of 128 tokens x 256
+// columns, and a pair of CTAs (cta_group::2) with 512 x 256.  It sweeps the
+// contraction in stages of 64:
+//   warp 0      TMA: the stage's tokens (128 x 64 bf16, 128-byte swizzle)
 //   warp 2      TMA: the stage's packed words, in a ring of their own
 //   warp 1      tensor memory and the MMAs (kind::f16, M 128, N 256, K 16)
 //   warps 3..18 dequantize the stage's 256 x 64 weights into a bf16 tile in
@@ -28,9 +28,8 @@
 //           writes 64 codes of one row as 128 bytes, which now is the MN-major
 //           layout of the same tile; the two matrices of the gated form are two
 //           sweeps into one accumulator.
-// Dequantization is arithmetic on two pipes (see weights8), about half of the
-// stage's 1024 MMA cycles.  A tile whose second 128 tokens lie past the end
-// skips that half's loads and MMAs.
+// Dequantization is arithmetic on two pipes (see weights8).  A pair's tile whose
+// second 256 tokens lie past the end skips their loads and MMAs.
 //
 // Tiles that do not fill the last wave of SMs split the contraction: their
 // partial tiles go to the workspace and a second kernel adds them in order and
@@ -48,17 +47,17 @@ namespace {
 
 enum Mode { kLinear, kGated, kBack };
 
-constexpr int TM = 256;                       // tokens per tile (two halves)
+constexpr int TM = 128;                       // tokens per tile of a single CTA
 constexpr int TN = 256;                       // tile columns (MMA N)
 constexpr int BK = 64;                        // contraction per stage
-constexpr int kAStages = 3;
-constexpr int kHalfBytes = 128 * BK * 2;      // 16 KB: one half's tokens
-constexpr int kABytes = 2 * kHalfBytes;
+constexpr int kAStages = 4;
+constexpr int kABytes = TM * BK * 2;          // 16 KB: a stage's tokens
 constexpr int kBBytes = TN * BK * 2;          // 32 KB: one dequantized tile
-constexpr int kMaxBBufs = 3, kMaxPStages = 6;
+constexpr int kBBufs = 4;
+constexpr int kMaxPStages = 6;
 constexpr int kDeqWarps = 16;                 // two groups of 8, each every other stage
 constexpr int kThreads = 32 * (3 + kDeqWarps);
-constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTmemCols = 256;
 constexpr int kSms = 148;                     // SMs of the device this library is built for
 constexpr int kMinStages = 8;                 // least stages of a split tile's part
 constexpr int kMaxSplit = 16;
@@ -73,15 +72,18 @@ struct Geom {
     static constexpr int kRowBytes = kBoxWords * 4;
     static constexpr bool kPairs = BITS == 3 && MODE != kBack;   // a slot serves two stages
     static constexpr int kSlot = MODE == kBack ? 64 * TN * BITS / 8 : TN * kRowBytes;
-    static constexpr int kPStages = BITS == 8 ? 3 : BITS == 4 ? 4 : BITS == 3 ? 2 : 6;
-    static constexpr int kBBufs = BITS == 8 ? 2 : 3;
+    static constexpr int kPStages = BITS == 8 ? 2 : BITS == 2 ? 6 : BITS == 3 && MODE != kBack ? 2 : 4;
     static constexpr int kSmem = kAStages * kABytes + kBBufs * kBBytes + kPStages * kSlot + 1024 + 256;
+    // a parity wait is only right for the phase after the last one seen, so a
+    // team has to meet every phase of a slot or buffer: stages it shares with
+    // the other team come back to it
+    static_assert((kPairs || kPStages % 2 == 0) && kBBufs % 2 == 0, "rings of whole rounds of two teams");
 };
 
 struct Bars {
     uint64_t afull[kAStages], aempty[kAStages];
     uint64_t pfull[kMaxPStages], pempty[kMaxPStages];
-    uint64_t bfull[kMaxBBufs], bempty[kMaxBBufs];
+    uint64_t bfull[kBBufs], bempty[kBBufs];
     uint64_t acc_full, drain;
     uint32_t tmem;
     int abort;
@@ -96,6 +98,7 @@ struct Args {
     int tiles_n, tiles_t;
     int full, split, per;   // whole tiles; parts of the others and their stages
     int part_rows;          // tokens of a partial tile
+    int tile_tokens;        // 256, or 512 per pair of CTAs
     float* part;
     const float* bias;
     int act;
@@ -254,6 +257,46 @@ __device__ __forceinline__ void weights8(const uint32_t (&w)[2 * BITS], int c, c
     }
 }
 
+// A CTA's accumulators (tokens t0 .. and t0 + step .. in the two halves) through
+// the epilogue, or into partial tile `slot` (whose rows start `row0` before t0).
+// Four warps share a lane quarter's chunks of 32 columns.
+template <int MODE>
+__device__ __forceinline__ void drain_tile(const Args& a, uint32_t tmem, int slot, int halves, int t0, int step,
+                                           int n0, int warp, int lane, int row0) {
+    const int q = warp & 3;           // tensor-memory lane quarter of this warp
+    const int side = (warp - 3) >> 2;
+    const int chunks = MODE == kGated && slot < 0 ? TN / 64 : TN / 32;
+#pragma unroll 1
+    for (int e = side; e < halves * chunks; e += kDeqWarps / 4) {
+        const int h = e / chunks, c = e % chunks;
+        const int t = t0 + h * step + 32 * q + lane;
+        const uint32_t at = tmem + (static_cast<uint32_t>(32 * q) << 16) + h * TN + c * 32;
+        float v[32], u[32];
+        tmem_ld32(at, v);
+        if constexpr (MODE == kGated) {
+            if (slot < 0) tmem_ld32(at + TN / 2, u);
+        }
+        if (t < a.n_tok && slot >= 0) {
+            float* p = a.part + (static_cast<int64_t>(slot) * a.part_rows + (t - t0 + row0)) * TN + c * 32;
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+                reinterpret_cast<float4*>(p)[x] = make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+        } else if (t < a.n_tok) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                float vv[8], uu[8];
+#pragma unroll
+                for (int y = 0; y < 8; ++y) {
+                    vv[y] = v[8 * x + y];
+                    uu[y] = MODE == kGated ? u[8 * x + y] : 0.f;
+                }
+                emit8<MODE>(a, t, n0 + c * 32 + 8 * x, vv, uu);
+            }
+        }
+        __syncwarp();
+    }
+}
+
 // GPT: groups in a thread's 64 codes (1 where g is a multiple of 64 or one group
 // spans the row).
 template <int BITS, int GPT, int MODE>
@@ -266,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
     uint8_t* bbuf = smem + kAStages * kABytes;
-    uint8_t* pbuf = bbuf + G::kBBufs * kBBytes;
+    uint8_t* pbuf = bbuf + kBBufs * kBBytes;
     Bars* bars = reinterpret_cast<Bars*>(pbuf + G::kPStages * G::kSlot);
     volatile int* abort = &bars->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -281,7 +324,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const int t0 = (tile / a.tiles_n) * TM;
     const int n0 = (tile % a.tiles_n) * (MODE == kGated ? TN / 2 : TN);
-    const int halves = t0 + 128 < a.n_tok ? 2 : 1;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kAStages; ++s) {
@@ -292,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bars->pfull[s], 1);
             mbar_init(&bars->pempty[s], G::kPairs ? kDeqWarps : kDeqWarps / 2);
         }
-        for (int b = 0; b < G::kBBufs; ++b) {
+        for (int b = 0; b < kBBufs; ++b) {
             mbar_init(&bars->bfull[b], kDeqWarps / 2);
             mbar_init(&bars->bempty[b], 1);
         }
@@ -322,9 +364,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool second = MODE == kBack && it >= a.nk1;
                 const CUtensorMap* map = second ? &tma1 : &tma0;
                 const int x = (second ? it - a.nk1 : it) * BK;
-                mbar_arrive_expect_tx(&bars->afull[st], halves * kHalfBytes);
-                for (int h = 0; h < halves; ++h)
-                    tma_load_2d(smem + st * kABytes + h * kHalfBytes, map, &bars->afull[st], x, t0 + 128 * h);
+                mbar_arrive_expect_tx(&bars->afull[st], kABytes);
+                tma_load_2d(smem + st * kABytes, map, &bars->afull[st], x, t0);
             }
             // never leave with copies in flight (bounded even when aborting)
             volatile int no_abort = 0;
@@ -375,25 +416,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr uint32_t kIdesc = instr_desc(/*bf16*/ 1, /*A K-major*/ 0, /*B*/ MODE == kBack ? 1 : 0, 128, TN);
             bool ok = true;
             for (int i = 0; i < k1 - k0; ++i) {
-                const int st = i % kAStages, b = i % G::kBBufs;
+                const int st = i % kAStages, b = i % kBBufs;
                 if (!mbar_wait_short(&bars->afull[st], (i / kAStages) & 1u, abort) ||
-                    !mbar_wait_short(&bars->bfull[b], (i / G::kBBufs) & 1u, abort)) {
+                    !mbar_wait_short(&bars->bfull[b], (i / kBBufs) & 1u, abort)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 const uint32_t am = smem_u32(smem + st * kABytes);
                 const uint32_t bm = smem_u32(bbuf + b * kBBytes);
-                for (int h = 0; h < halves; ++h)
 #pragma unroll
-                    for (int kk = 0; kk < BK / 16; ++kk) {
-                        // K-major: 32 bytes of each row; MN-major: two atoms of 8
-                        // weight rows, boxes of 64 columns 8 KB apart
-                        const uint64_t bd = MODE == kBack ? smem_desc(bm + kk * 2048, 8192, 1024, 2)
-                                                          : smem_desc(bm + kk * 32, 16, 1024, 2);
-                        mma_f16_ss(tmem + h * TN, smem_desc(am + h * kHalfBytes + kk * 32, 16, 1024, 2), bd, kIdesc,
-                                   (i > 0 || kk > 0) ? 1u : 0u);
-                    }
+                for (int kk = 0; kk < BK / 16; ++kk) {
+                    // K-major: 32 bytes of each row; MN-major: two atoms of 8
+                    // weight rows, boxes of 64 columns 8 KB apart
+                    const uint64_t bd = MODE == kBack ? smem_desc(bm + kk * 2048, 8192, 1024, 2)
+                                                      : smem_desc(bm + kk * 32, 16, 1024, 2);
+                    mma_f16_ss(tmem, smem_desc(am + kk * 32, 16, 1024, 2), bd, kIdesc, (i > 0 || kk > 0) ? 1u : 0u);
+                }
                 mma_commit(&bars->aempty[st]);
                 mma_commit(&bars->bempty[b]);
             }
@@ -457,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         for (int it = k0 + team, i = team; it < k1; it += 2, i += 2) {
             const int pi = G::kPairs ? i >> 1 : i;
-            const int ps = pi % G::kPStages, b = i % G::kBBufs;
+            const int ps = pi % G::kPStages, b = i % kBBufs;
 #pragma unroll
             for (int q = 0; q < GPT; ++q) {
                 s[q] = s_nx[q];
@@ -479,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             uint32_t w[2 * BITS];
             load_words<BITS>(src, w);
-            if (!mbar_wait_short(&bars->bempty[b], ((i / G::kBBufs) & 1u) ^ 1u, abort)) {
+            if (!mbar_wait_short(&bars->bempty[b], ((i / kBBufs) & 1u) ^ 1u, abort)) {
                 ok = false;
                 break;
             }
@@ -505,38 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------ drain: tensor memory -> output
         if (ok && mbar_wait_short(&bars->acc_full, 0, abort)) {
             tc_fence_after();
-            const int q = warp & 3;           // tensor-memory lane quarter of this warp
-            const int side = (warp - 3) >> 2; // it shares the quarter's chunks with three other warps
-            const int chunks = MODE == kGated && slot < 0 ? TN / 64 : TN / 32;
-#pragma unroll 1
-            for (int e = side; e < halves * chunks; e += kDeqWarps / 4) {
-                const int h = e / chunks, c = e % chunks;
-                const int t = t0 + h * 128 + 32 * q + lane;
-                const uint32_t at = tmem + (static_cast<uint32_t>(32 * q) << 16) + h * TN + c * 32;
-                float v[32], u[32];
-                tmem_ld32(at, v);
-                if constexpr (MODE == kGated) {
-                    if (slot < 0) tmem_ld32(at + TN / 2, u);
-                }
-                if (t < a.n_tok && slot >= 0) {
-                    float* p = a.part + (static_cast<int64_t>(slot) * a.part_rows + (t - t0)) * TN + c * 32;
-#pragma unroll
-                    for (int x = 0; x < 8; ++x)
-                        reinterpret_cast<float4*>(p)[x] = make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
-                } else if (t < a.n_tok) {
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        float vv[8], uu[8];
-#pragma unroll
-                        for (int y = 0; y < 8; ++y) {
-                            vv[y] = v[8 * x + y];
-                            uu[y] = MODE == kGated ? u[8 * x + y] : 0.f;
-                        }
-                        emit8<MODE>(a, t, n0 + c * 32 + 8 * x, vv, uu);
-                    }
-                }
-                __syncwarp();
-            }
+            drain_tile<MODE>(a, tmem, slot, 1, t0, 0, n0, warp, lane, 0);
         }
     }
 
@@ -544,6 +552,324 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+    if (threadIdx.x == 0 && bars->abort) report(a.status, GPTQ_ERR_TIMEOUT);
+}
+
+// ------------------------------------------------------------ pairs of CTAs
+// The same product by two CTAs of a cluster (cta_group::2): a tile of 512 tokens
+// x 256 columns, MMAs of M 256 (128 tokens of each CTA) and N 256, of whose
+// weight rows each CTA dequantizes and holds 128 (gated: one the gate's, the
+// other the up matrix's; backward: 128 of the columns k).  Against two single
+// CTAs the weight tile is dequantized, written and read once instead of twice:
+// 120 KB of shared memory traffic per CTA and stage instead of 176, at 128 bytes
+// per cycle the difference between 940 and 1375 cycles for 1024 of MMAs.
+// Roles as above, with four teams of four dequantizing warps (one thread per 64
+// codes of one of the CTA's 128 rows).  The teams of both CTAs report a stage to
+// rank 0's barrier, and one thread of rank 1 its tokens' arrival.  A thread
+// meets every phase of a barrier that it waits on, in order: a parity wait for
+// phase n returns at once while phase n - 1 is still open.
+constexpr int kTeams = 4;
+constexpr int PM = 512;                       // tokens per pair and tile
+constexpr int kPairBBytes = 128 * BK * 2;     // 16 KB: a CTA's half of the weight tile
+constexpr int kPairAStages = 3;
+constexpr int kHalfBytes = 128 * BK * 2;      // 16 KB: 128 tokens of a stage
+constexpr int kPairABytes = 2 * kHalfBytes;
+constexpr uint32_t kPairTmemCols = 512;
+template <int BITS, int MODE>
+struct PairGeom {
+    static constexpr int kBoxWords = Geom<BITS, MODE>::kBoxWords;
+    static constexpr int kRowBytes = Geom<BITS, MODE>::kRowBytes;
+    static constexpr bool kPairs = Geom<BITS, MODE>::kPairs;
+    static constexpr int kSlot = Geom<BITS, MODE>::kSlot / 2;
+    static constexpr int kPStages = BITS == 8 ? 4 : BITS == 3 && MODE != kBack ? 4 : 8;
+    static constexpr int kBBufs = kTeams;   // a team's own: it meets every phase of its barriers
+    static constexpr int kSmem = kPairAStages * kPairABytes + kBBufs * kPairBBytes + kPStages * kSlot + 1024 + 512;
+    static_assert((kPairs ? 2 * kPStages : kPStages) % kTeams == 0, "rings of whole rounds of the teams");
+};
+struct PairBars {
+    uint64_t afull[kPairAStages], aempty[kPairAStages];
+    uint64_t peer[kPairAStages];                // rank 0's: rank 1's tokens have landed
+    uint64_t pfull[8], pempty[8];
+    uint64_t ready[kTeams], bempty[kTeams];     // ready: rank 0's, arrivals of both CTAs
+    uint64_t acc_full, drain;
+    uint32_t tmem;
+    int abort;
+};
+
+template <int BITS, int GPT, int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    pair_gemm_kernel(const __grid_constant__ CUtensorMap tma0, const __grid_constant__ CUtensorMap tma1,
+                     const __grid_constant__ CUtensorMap tmp0, const __grid_constant__ CUtensorMap tmp1,
+                     const __grid_constant__ Args a) {
+    using G = PairGeom<BITS, MODE>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    uint8_t* bbuf = smem + kPairAStages * kPairABytes;
+    uint8_t* pbuf = bbuf + G::kBBufs * kPairBBytes;
+    PairBars* bars = reinterpret_cast<PairBars*>(pbuf + G::kPStages * G::kSlot);
+    volatile int* abort = &bars->abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = static_cast<int>(cluster_rank());
+
+    int tile = blockIdx.x >> 1, k0 = 0, k1 = a.nk, slot = -1;
+    if (tile >= a.full) {
+        slot = tile - a.full;
+        tile = a.full + slot / a.split;
+        k0 = (slot % a.split) * a.per;
+        k1 = min(a.nk, k0 + a.per);
+    }
+    const int t0 = (tile / a.tiles_n) * PM + 128 * rank;     // this CTA's tokens: t0 .. and t0 + 256 ..
+    const int n0 = (tile % a.tiles_n) * (MODE == kGated ? TN / 2 : TN);
+    const int halves = (tile / a.tiles_n) * PM + 256 < a.n_tok ? 2 : 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kPairAStages; ++s) {
+            mbar_init(&bars->afull[s], 1);
+            mbar_init(&bars->aempty[s], 1);
+            mbar_init(&bars->peer[s], 1);
+        }
+        for (int s = 0; s < G::kPStages; ++s) {
+            mbar_init(&bars->pfull[s], 1);
+            mbar_init(&bars->pempty[s], G::kPairs ? 8 : 4);
+        }
+        for (int b = 0; b < G::kBBufs; ++b) {
+            mbar_init(&bars->ready[b], 8);
+            mbar_init(&bars->bempty[b], 1);
+        }
+        mbar_init(&bars->acc_full, 1);
+        mbar_init(&bars->drain, 1);
+        bars->abort = 0;
+        fence_barrier_init();
+        tma_prefetch_desc(&tma0);
+        tma_prefetch_desc(&tmp0);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(&bars->tmem, kPairTmemCols);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();   // both CTAs' barriers are there
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem;
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA: tokens
+        if (lane == 0) {
+            int i = 0;
+            for (int it = k0; it < k1 && !*abort; ++it, ++i) {
+                const int st = i % kPairAStages;
+                if (!mbar_wait_short(&bars->aempty[st], ((i / kPairAStages) & 1u) ^ 1u, abort)) break;
+                const bool second = MODE == kBack && it >= a.nk1;
+                const CUtensorMap* map = second ? &tma1 : &tma0;
+                const int x = (second ? it - a.nk1 : it) * BK;
+                mbar_arrive_expect_tx(&bars->afull[st], halves * kHalfBytes);
+                for (int h = 0; h < halves; ++h)
+                    tma_load_2d(smem + st * kPairABytes + h * kHalfBytes, map, &bars->afull[st], x, t0 + 256 * h);
+            }
+            // never leave with copies in flight (bounded even when aborting)
+            volatile int no_abort = 0;
+            for (int j = 0; j < min(i, kPairAStages); ++j) {
+                const int i2 = i - 1 - j;
+                if (!mbar_wait_short(&bars->afull[i2 % kPairAStages], (i2 / kPairAStages) & 1u, &no_abort)) {
+                    *abort = 1;
+                    break;
+                }
+            }
+        }
+    } else if (warp == 2) {
+        // ------------------------------------------------ TMA: packed words
+        if (lane == 0) {
+            constexpr int kStep = G::kPairs ? 2 : 1;
+            const CUtensorMap* own = MODE == kGated && rank == 1 ? &tmp1 : &tmp0;
+            const int row0 = MODE == kGated ? n0 : n0 + 128 * rank;
+            int i = 0;
+            for (int it = k0; it < k1 && !*abort; it += kStep, ++i) {
+                const int ps = i % G::kPStages;
+                if (!mbar_wait_short(&bars->pempty[ps], ((i / G::kPStages) & 1u) ^ 1u, abort)) break;
+                uint8_t* dst = pbuf + ps * G::kSlot;
+                mbar_arrive_expect_tx(&bars->pfull[ps], G::kSlot);
+                if constexpr (MODE == kBack) {
+                    const bool second = it >= a.nk1;
+                    const int row = (second ? it - a.nk1 : it) * BK;
+                    constexpr int kBoxCodes = Geom<BITS, MODE>::kBoxCodes, kBoxes = 128 / kBoxCodes;
+                    for (int c = 0; c < kBoxes; ++c)
+                        tma_load_2d(dst + c * (BK * G::kRowBytes), second ? &tmp1 : &tmp0, &bars->pfull[ps],
+                                    (row0 / kBoxCodes + c) * G::kBoxWords, row);
+                } else {
+                    tma_load_2d(dst, own, &bars->pfull[ps], (it / kStep) * G::kBoxWords, row0);
+                }
+            }
+            volatile int no_abort = 0;
+            for (int j = 0; j < min(i, G::kPStages); ++j) {
+                const int i2 = i - 1 - j;
+                if (!mbar_wait_short(&bars->pfull[i2 % G::kPStages], (i2 / G::kPStages) & 1u, &no_abort)) {
+                    *abort = 1;
+                    break;
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer (for both CTAs)
+        if (lane == 0 && rank == 0) {
+            constexpr uint32_t kIdesc = instr_desc(/*bf16*/ 1, /*A K-major*/ 0, /*B*/ MODE == kBack ? 1 : 0, 256, TN);
+            bool ok = true;
+            for (int i = 0; i < k1 - k0; ++i) {
+                const int st = i % kPairAStages, b = i % G::kBBufs;
+                if (!mbar_wait_short(&bars->afull[st], (i / kPairAStages) & 1u, abort) ||
+                    !mbar_wait_cluster(&bars->peer[st], (i / kPairAStages) & 1u, abort) ||
+                    !mbar_wait_cluster(&bars->ready[b], (i / G::kBBufs) & 1u, abort)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t am = smem_u32(smem + st * kPairABytes);
+                const uint32_t bm = smem_u32(bbuf + b * kPairBBytes);
+                for (int h = 0; h < halves; ++h)
+#pragma unroll
+                    for (int kk = 0; kk < BK / 16; ++kk) {
+                        // as in the single-CTA kernel, each CTA with its 128 rows of both
+                        const uint64_t bd = MODE == kBack ? smem_desc(bm + kk * 2048, 8192, 1024, 2)
+                                                          : smem_desc(bm + kk * 32, 16, 1024, 2);
+                        mma_f16_ss_pair(tmem + h * TN, smem_desc(am + h * kHalfBytes + kk * 32, 16, 1024, 2), bd, kIdesc,
+                                        (i > 0 || kk > 0) ? 1u : 0u);
+                    }
+                mma_commit_pair(&bars->aempty[st]);
+                mma_commit_pair(&bars->bempty[b]);
+            }
+            if (ok) mma_commit_pair(&bars->acc_full);
+            mma_commit_pair(&bars->drain);
+            volatile int no_abort = 0;
+            if (!mbar_wait_short(&bars->drain, 0, &no_abort)) *abort = 1;
+        } else if (lane == 0) {
+            // rank 1: passes its tokens' arrival on, in order
+            bool ok = true;
+            for (int i = 0; i < k1 - k0 && ok; ++i) {
+                const int st = i % kPairAStages;
+                ok = mbar_wait_short(&bars->afull[st], (i / kPairAStages) & 1u, abort);
+                if (ok) mbar_arrive_cluster(&bars->peer[st], 0);
+            }
+            // the last arrivals that rank 0's MMAs send here have to land before this CTA leaves
+            volatile int no_abort = 0;
+            if (!mbar_wait_short(&bars->drain, 0, &no_abort)) *abort = 1;
+            for (int d = 0; ok && d < kPairAStages && d < k1 - k0; ++d) {
+                const int i = k1 - k0 - 1 - d;
+                mbar_wait_short(&bars->aempty[i % kPairAStages], (i / kPairAStages) & 1u, abort);
+            }
+            for (int d = 0; ok && d < G::kBBufs && d < k1 - k0; ++d) {
+                const int i = k1 - k0 - 1 - d;
+                mbar_wait_short(&bars->bempty[i % G::kBBufs], (i / G::kBBufs) & 1u, abort);
+            }
+        }
+    } else {
+        // ------------------------------------------------ dequantize
+        const int j = (threadIdx.x - 96) & 127;   // the thread's 128 bytes of the CTA's half of the tile
+        const int team = (threadIdx.x - 96) >> 7;
+        const int mi = MODE == kGated ? rank : 0;
+        const int wrow = n0 + (MODE == kGated ? 0 : 128 * rank) + j;             // forward
+        const int kcol = n0 + 128 * rank + 64 * (j >> 6);                        // backward
+        const int groups = (a.d_col + a.g - 1) / a.g;
+        float s[GPT] = {}, s_nx[GPT];
+        int z[GPT] = {}, z_nx[GPT];
+        const int span = GPT == 1 ? a.g / BK : 1;
+        int gi = GPT == 1 && MODE != kBack ? (k0 + team) / span : 0, rem = GPT == 1 && MODE != kBack ? (k0 + team) % span : 0;
+        const int back_group = GPT == 1 ? kcol / a.g : kcol / 64 * GPT;
+        auto fetch = [&](int it) {
+#pragma unroll
+            for (int q = 0; q < GPT; ++q) {
+                int group, row, m;
+                bool in;
+                if constexpr (MODE == kBack) {
+                    m = it >= a.nk1 ? 1 : 0;
+                    row = (m ? it - a.nk1 : it) * BK + (j & 63);
+                    group = back_group + q;
+                    in = it < k1 && row < a.d_row && kcol < a.d_col;
+                } else {
+                    m = mi;
+                    row = wrow;
+                    group = GPT == 1 ? gi : it * GPT + q;
+                    in = it < k1 && row < a.d_row && group < groups;
+                }
+                s_nx[q] = 0.f;   // rows and columns past the layer: weights 0
+                z_nx[q] = 0;
+                if (in) {
+                    const int64_t at = static_cast<int64_t>(group) * a.d_row + row;
+                    s_nx[q] = __ldg(a.mat[m].scales + at);
+                    z_nx[q] = __ldg(a.mat[m].zeros + at);
+                }
+            }
+            if constexpr (GPT == 1 && MODE != kBack) {   // the group four stages on
+                rem += kTeams;
+                while (rem >= span) {
+                    rem -= span;
+                    ++gi;
+                }
+            }
+        };
+        fetch(k0 + team);
+        Group<BITS> grp;
+        uint32_t dst_off[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) dst_off[c] = j * 128 + ((c ^ (j & 7)) << 4);
+        bool ok = true;
+        for (int it = k0 + team, i = team; it < k1; it += kTeams, i += kTeams) {
+            const int pi = G::kPairs ? i >> 1 : i;
+            const int ps = pi % G::kPStages, b = i % G::kBBufs;
+#pragma unroll
+            for (int q = 0; q < GPT; ++q) {
+                s[q] = s_nx[q];
+                z[q] = z_nx[q];
+            }
+            fetch(it + kTeams);
+            if constexpr (GPT == 1) grp.set(s[0], static_cast<float>(z[0]));
+            if (!mbar_wait_short(&bars->pfull[ps], (pi / G::kPStages) & 1u, abort)) {
+                ok = false;
+                break;
+            }
+            const uint8_t* src = pbuf + ps * G::kSlot;
+            if constexpr (BITS != 3) {
+                src += j * G::kRowBytes;
+            } else if constexpr (MODE == kBack) {
+                src += (j & 63) * G::kRowBytes + (j >> 6) * (G::kRowBytes / 2);
+            } else {
+                src += j * G::kRowBytes + (i & 1) * (G::kRowBytes / 2);
+            }
+            uint32_t w[2 * BITS];
+            load_words<BITS>(src, w);
+            if (!mbar_wait_short(&bars->bempty[b], ((i / G::kBBufs) & 1u) ^ 1u, abort)) {
+                ok = false;
+                break;
+            }
+            const uint32_t tile_at = smem_u32(bbuf + b * kPairBBytes);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                if constexpr (GPT > 1) {
+                    if (c % (8 / GPT) == 0) grp.set(s[c / (8 / GPT)], static_cast<float>(z[c / (8 / GPT)]));
+                }
+                uint32_t o[4];
+                weights8<BITS>(w, c, grp, o);
+                sts128_u(tile_at + dst_off[c], make_uint4(o[0], o[1], o[2], o[3]));
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive_cluster(&bars->ready[b], 0);
+                mbar_arrive(&bars->pempty[ps]);
+            }
+        }
+        // ------------------------------------------------ drain: tensor memory -> output
+        if (ok && mbar_wait_short(&bars->acc_full, 0, abort)) {
+            tc_fence_after();
+            drain_tile<MODE>(a, tmem, slot, halves, t0, 256, n0, warp, lane, 128 * rank);
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();   // no CTA leaves while the pair's MMAs or arrivals may touch it
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc_pair(tmem, kPairTmemCols);
     if (threadIdx.x == 0 && bars->abort) report(a.status, GPTQ_ERR_TIMEOUT);
 }
 
@@ -558,7 +884,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
         const int i = static_cast<int>(e / per_tile), r = static_cast<int>(e % per_tile);
         const int row = r / (kOut / 8), c = (r % (kOut / 8)) * 8;
         const int tile = a.full + i;
-        const int t = (tile / a.tiles_n) * TM + row, n = (tile % a.tiles_n) * kOut + c;
+        const int t = (tile / a.tiles_n) * a.tile_tokens + row, n = (tile % a.tiles_n) * kOut + c;
         if (t >= a.n_tok || n >= a.N) continue;
         float v[8] = {}, u[8] = {};
         for (int k = 0; k < a.split; ++k) {
@@ -580,23 +906,31 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
 // Tiles of the output, how many of them run whole, and into how many parts of
 // `per` stages each of the others is split.
 struct Plan {
-    int tiles_n, tiles_t, full, split, per, part_rows;
+    bool pair;      // pairs of CTAs with tiles of 512 tokens
+    int tile_tokens, tiles_n, tiles_t, full, split, per, part_rows;
     size_t part_bytes;
 };
+
+// Pairs of CTAs from here on: below, half of a pair's 256 token rows would be
+// empty, and single CTAs with one half tile spread the weights over more SMs.
+constexpr int kPairTokens = 129;
 
 Plan make_plan(int64_t n_tok, int64_t N, int nk, bool gated, bool pairs) {
     Plan p;
     const int out = gated ? TN / 2 : TN;
     p.tiles_n = static_cast<int>((N + out - 1) / out);
-    p.tiles_t = static_cast<int>((n_tok + TM - 1) / TM);
+    p.pair = n_tok >= kPairTokens;
+    p.tile_tokens = p.pair ? PM : TM;
+    const int slots = p.pair ? kSms / 2 : kSms;
+    p.tiles_t = static_cast<int>((n_tok + p.tile_tokens - 1) / p.tile_tokens);
     const int64_t tiles = static_cast<int64_t>(p.tiles_n) * p.tiles_t;
     p.full = static_cast<int>(tiles);
     p.split = 1;
     p.per = nk;
-    p.part_rows = static_cast<int>(n_tok < TM ? n_tok : TM);
+    p.part_rows = static_cast<int>(n_tok < p.tile_tokens ? n_tok : p.tile_tokens);
     p.part_bytes = 0;
-    const int rest = static_cast<int>(tiles % kSms);
-    int split = rest > 0 ? kSms / rest : 1;
+    const int rest = static_cast<int>(tiles % slots);
+    int split = rest > 0 ? slots / rest : 1;
     if (split > kMaxSplit) split = kMaxSplit;
     if (split > nk / kMinStages) split = nk / kMinStages;
     if (split > 1) {
@@ -616,12 +950,14 @@ Plan make_plan(int64_t n_tok, int64_t N, int nk, bool gated, bool pairs) {
 template <int BITS, int GPT, int MODE>
 cudaError_t launch_one(const CUtensorMap (&ta)[2], const CUtensorMap (&tp)[2], const Args& a, int units,
                        cudaStream_t stream) {
-    auto kern = packed_gemm_kernel<BITS, GPT, MODE>;
-    constexpr int kSmem = Geom<BITS, MODE>::kSmem;
-    static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    const bool pair = a.tile_tokens == PM;
+    auto kern = pair ? pair_gemm_kernel<BITS, GPT, MODE> : packed_gemm_kernel<BITS, GPT, MODE>;
+    const int smem = pair ? PairGeom<BITS, MODE>::kSmem : Geom<BITS, MODE>::kSmem;
+    static_assert(PairGeom<BITS, MODE>::kSmem <= 227 * 1024 && Geom<BITS, MODE>::kSmem <= 227 * 1024,
+                  "shared memory per CTA");
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kern<<<units, kThreads, kSmem, stream>>>(ta[0], ta[1], tp[0], tp[1], a);
+    kern<<<pair ? 2 * units : units, kThreads, smem, stream>>>(ta[0], ta[1], tp[0], tp[1], a);
     return cudaGetLastError();
 }
 
@@ -641,6 +977,7 @@ gptq_status run(Args a, const CUtensorMap (&ta)[2], const uint32_t* const (&pack
     const Plan p = make_plan(a.n_tok, a.N, a.nk, MODE == kGated, pairs);
     a.tiles_n = p.tiles_n; a.tiles_t = p.tiles_t;
     a.full = p.full; a.split = p.split; a.per = p.per; a.part_rows = p.part_rows;
+    a.tile_tokens = p.tile_tokens;
     a.part = static_cast<float*>(part);
     const int rest = p.tiles_n * p.tiles_t - p.full;
     const int units = p.full + rest * p.split;
