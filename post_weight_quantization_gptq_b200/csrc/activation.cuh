@@ -5,7 +5,7 @@
 // 1 + erf and 1 + tanh).  exp and the quotient are CUDA's approximate forms: a
 // few units of 2^-23 plus the rounding of exp's argument, against 2^-8 of the
 // bf16 outputs (with the exact forms a 256 x 256 output tile spent 56 us in its
-// GELU, almost half of what its product takes).
+// GELU, almost half of what its product takes; 16 us with one branch per value).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -19,17 +19,21 @@ constexpr float kInvSqrt2 = 0.70710678118654752440f;
 constexpr float kInvSqrt2Pi = 0.39894228040143267794f;
 constexpr float kGeluCubic = 0.044715f;
 
-// 1 / (1 + exp(-x)); exp(-x) overflows to +inf for x < -88: 0 then
-__device__ __forceinline__ float sigmoid_f(float x) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-x)));
+constexpr float kLog2E = 1.44269504088896340736f;
+
+// 1 / (1 + 2^y); 2^y overflows to +inf beyond y = 128: 0 then
+__device__ __forceinline__ float inv_one_plus_exp2(float y) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(y));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
     return r;
 }
+__device__ __forceinline__ float sigmoid_f(float x) { return inv_one_plus_exp2(-kLog2E * x); }
 
 // (1 + tanh(u)) / 2 = 1 / (1 + exp(-2u)), u = sqrt(2/pi) (x + 0.044715 x^3)
 __device__ __forceinline__ float gelu_tanh_half(float x) {
-    const float u = kSqrt2OverPi * (x + kGeluCubic * x * x * x);
-    return sigmoid_f(2.f * u);
+    constexpr float k1 = -2.f * kLog2E * kSqrt2OverPi, k3 = k1 * kGeluCubic;
+    return inv_one_plus_exp2(x * fmaf(k3, x * x, k1));
 }
 
 __device__ __forceinline__ float activate(float x, int act) {
@@ -39,6 +43,30 @@ __device__ __forceinline__ float activate(float x, int act) {
         case GPTQ_ACT_GELU_TANH: return x * gelu_tanh_half(x);
         case GPTQ_ACT_SILU: return x * sigmoid_f(x);
         default: return x;
+    }
+}
+
+// N values at once (one branch on the activation)
+template <int N>
+__device__ __forceinline__ void activate_all(float (&v)[N], int act) {
+    switch (act) {
+        case GPTQ_ACT_RELU:
+#pragma unroll
+            for (int j = 0; j < N; ++j) v[j] = activate(v[j], GPTQ_ACT_RELU);
+            break;
+        case GPTQ_ACT_GELU:
+#pragma unroll
+            for (int j = 0; j < N; ++j) v[j] = activate(v[j], GPTQ_ACT_GELU);
+            break;
+        case GPTQ_ACT_GELU_TANH:
+#pragma unroll
+            for (int j = 0; j < N; ++j) v[j] = activate(v[j], GPTQ_ACT_GELU_TANH);
+            break;
+        case GPTQ_ACT_SILU:
+#pragma unroll
+            for (int j = 0; j < N; ++j) v[j] = activate(v[j], GPTQ_ACT_SILU);
+            break;
+        default: break;
     }
 }
 

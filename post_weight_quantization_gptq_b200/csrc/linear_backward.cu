@@ -19,11 +19,12 @@ namespace {
 constexpr int kCols = 256;      // columns per CTA: 32 lanes x 8
 constexpr int kRows = 8;        // token rows in flight per CTA
 constexpr int kMaxSlabs = 256;  // token slabs of the bias sums
+constexpr int kSlab = 16;       // tokens of one, at least
 
-// Tokens per CTA: 32, or as many as leave at most kMaxSlabs slabs.
+// Tokens per CTA: kSlab, or as many as leave at most kMaxSlabs slabs.
 int64_t slab_tokens(int64_t n_tok) {
     const int64_t least = (n_tok + kMaxSlabs - 1) / kMaxSlabs;
-    return least <= 32 ? 32 : (least + kRows - 1) / kRows * kRows;
+    return least <= kSlab ? kSlab : (least + kRows - 1) / kRows * kRows;
 }
 int64_t slabs(int64_t n_tok) { return (n_tok + slab_tokens(n_tok) - 1) / slab_tokens(n_tok); }
 
@@ -53,10 +54,51 @@ __device__ __forceinline__ void put8(uint16_t* p, const float (&v)[8], int count
     }
 }
 
+// (act(x), act'(x)) of eight values (one branch on the activation).
+template <bool VALUE>
+__device__ __forceinline__ void slopes8(const float (&x)[8], float (&value)[8], float (&slope)[8], int act) {
+    auto each = [&](int which) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            slope[j] = activate_slope(x[j], which);
+            if constexpr (VALUE) value[j] = activate(x[j], which);
+        }
+    };
+    switch (act) {
+        case GPTQ_ACT_RELU: each(GPTQ_ACT_RELU); break;
+        case GPTQ_ACT_GELU: each(GPTQ_ACT_GELU); break;
+        case GPTQ_ACT_GELU_TANH: each(GPTQ_ACT_GELU_TANH); break;
+        case GPTQ_ACT_SILU: each(GPTQ_ACT_SILU); break;
+        default: each(GPTQ_ACT_NONE); break;
+    }
+}
+
 // The outputs may be the inputs themselves: a thread reads its eight entries
-// of all of them before it writes.
-template <bool GATED>
-__global__ void __launch_bounds__(256) slopes_kernel(const BackwardCall c, float* bias_part, int64_t slab) {
+// of all of them before it writes.  A warp takes 256 columns of a token.
+__global__ void __launch_bounds__(256) gated_slopes_kernel(const __grid_constant__ BackwardCall c, int chunks) {
+    const int lane = threadIdx.x & 31;
+    const int64_t total = c.n_tok * chunks;
+    for (int64_t e = blockIdx.x * 8ll + (threadIdx.x >> 5); e < total; e += gridDim.x * 8ll) {
+        const int64_t t = e / chunks, n = (e - t * chunks) * kCols + 8 * lane;
+        const int count = static_cast<int>(c.d_row - n < 8 ? c.d_row - n : 8);
+        if (count <= 0) continue;
+        float dy[8], g[8], u[8], value[8], slope[8];
+        get8(c.dY + t * c.lddy + n, dy, count);
+        get8(c.pre[0] + t * c.ldpre[0] + n, g, count);
+        get8(c.pre[1] + t * c.ldpre[1] + n, u, count);
+        slopes8<true>(g, value, slope, c.act);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            u[j] = dy[j] * u[j] * slope[j];
+            g[j] = dy[j] * value[j];
+        }
+        put8(c.dP[0] + t * c.lddp[0] + n, u, count);
+        put8(c.dP[1] + t * c.lddp[1] + n, g, count);
+    }
+}
+
+// A CTA takes a slab of tokens of 256 columns and leaves the columns' sums.
+__global__ void __launch_bounds__(256) slopes_kernel(const __grid_constant__ BackwardCall c, float* bias_part, int64_t slab) {
     __shared__ float sums[kRows][kCols + 8];
     const int lane = threadIdx.x & 31, r = threadIdx.x >> 5;
     const int64_t n = blockIdx.x * static_cast<int64_t>(kCols) + 8 * lane;
@@ -68,42 +110,28 @@ __global__ void __launch_bounds__(256) slopes_kernel(const BackwardCall c, float
         for (int64_t t = blockIdx.y * slab + r; t < t1; t += kRows) {
             float dy[8];
             get8(c.dY + t * c.lddy + n, dy, count);
-            if constexpr (GATED) {
-                float g[8], u[8];
-                get8(c.pre[0] + t * c.ldpre[0] + n, g, count);
-                get8(c.pre[1] + t * c.ldpre[1] + n, u, count);
+            if (c.act != GPTQ_ACT_NONE) {
+                float p[8], slope[8];
+                get8(c.pre[0] + t * c.ldpre[0] + n, p, count);
+                slopes8<false>(p, p, slope, c.act);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    u[j] = dy[j] * u[j] * activate_slope(g[j], c.act);
-                    g[j] = dy[j] * activate(g[j], c.act);
-                }
-                put8(c.dP[0] + t * c.lddp[0] + n, u, count);
-                put8(c.dP[1] + t * c.lddp[1] + n, g, count);
-            } else {
-                if (c.act != GPTQ_ACT_NONE) {
-                    float p[8];
-                    get8(c.pre[0] + t * c.ldpre[0] + n, p, count);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) dy[j] *= activate_slope(p[j], c.act);
-                }
-                if (c.dP[0] != nullptr) put8(c.dP[0] + t * c.lddp[0] + n, dy, count);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) sum[j] += dy[j];
+                for (int j = 0; j < 8; ++j) dy[j] *= slope[j];
             }
+            if (c.dP[0] != nullptr) put8(c.dP[0] + t * c.lddp[0] + n, dy, count);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum[j] += dy[j];
         }
     }
-    if constexpr (!GATED) {
-        if (bias_part == nullptr) return;
+    if (bias_part == nullptr) return;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sums[r][8 * lane + j] = sum[j];
-        __syncthreads();
-        const int64_t col = blockIdx.x * static_cast<int64_t>(kCols) + threadIdx.x;
-        if (col < c.d_row) {
-            float v = 0.f;
+    for (int j = 0; j < 8; ++j) sums[r][8 * lane + j] = sum[j];
+    __syncthreads();
+    const int64_t col = blockIdx.x * static_cast<int64_t>(kCols) + threadIdx.x;
+    if (col < c.d_row) {
+        float v = 0.f;
 #pragma unroll
-            for (int q = 0; q < kRows; ++q) v += sums[q][threadIdx.x];
-            bias_part[blockIdx.y * c.d_row + col] = v;
-        }
+        for (int q = 0; q < kRows; ++q) v += sums[q][threadIdx.x];
+        bias_part[blockIdx.y * c.d_row + col] = v;
     }
 }
 
@@ -180,10 +208,15 @@ size_t bias_partial_bytes(int64_t n_tok, int64_t d_row) {
 gptq_status launch_slopes(const BackwardCall& c, float* bias_part, int64_t* launches, cudaStream_t stream) {
     const bool gated = c.mat[1].packed != nullptr;
     if (!gated && c.dP[0] == nullptr && bias_part == nullptr) return GPTQ_OK;   // dY is the gradient
-    const int64_t ns = slabs(c.n_tok);
-    const dim3 grid(static_cast<unsigned>((c.d_row + kCols - 1) / kCols), static_cast<unsigned>(ns));
-    if (gated) slopes_kernel<true><<<grid, 256, 0, stream>>>(c, nullptr, slab_tokens(c.n_tok));
-    else slopes_kernel<false><<<grid, 256, 0, stream>>>(c, bias_part, slab_tokens(c.n_tok));
+    const int64_t ns = slabs(c.n_tok), chunks = (c.d_row + kCols - 1) / kCols;
+    if (gated) {
+        const int64_t want = (c.n_tok * chunks + 7) / 8, most = 8 * num_sms();
+        gated_slopes_kernel<<<static_cast<unsigned>(want < most ? want : most), 256, 0, stream>>>(
+            c, static_cast<int>(chunks));
+    } else {
+        slopes_kernel<<<dim3(static_cast<unsigned>(chunks), static_cast<unsigned>(ns)), 256, 0, stream>>>(
+            c, bias_part, slab_tokens(c.n_tok));
+    }
     if (cudaGetLastError() != cudaSuccess) return GPTQ_ERR_CUDA;
     ++*launches;
     if (bias_part != nullptr) {

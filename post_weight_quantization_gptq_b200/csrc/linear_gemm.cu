@@ -112,77 +112,108 @@ struct Args {
 };
 
 // ------------------------------------------------------------- epilogue
-__device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8], int count) {
-    if (count == 8 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-        *reinterpret_cast<uint4*>(p) = make_uint4(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]),
-                                                  f32x2_to_bf16x2(v[4], v[5]), f32x2_to_bf16x2(v[6], v[7]));
+// Sixteen consecutive bf16 values (32 bytes, the sector that L2 moves): in one
+// access where the address allows it, else in smaller ones.
+__device__ __forceinline__ void store16(uint16_t* p, const float (&v)[16], int count) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    uint32_t w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = f32x2_to_bf16x2(v[2 * j], v[2 * j + 1]);
+    if (count == 16 && (at & 31) == 0) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
+                     "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else if (count == 16 && (at & 15) == 0) {
+        reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < count) p[j] = f32_to_bf16_bits(v[j]);
+        for (int j = 0; j < 16; ++j)
+            if (j < count) p[j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
     }
 }
-__device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8], int count) {
-    if (count == 8 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-        const uint4 q = *reinterpret_cast<const uint4*>(p);
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[2 * j] = __uint_as_float(w[j] << 16);
-            v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-        }
+__device__ __forceinline__ void load16(const uint16_t* p, uint32_t (&w)[8], int count) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    if (count == 16 && (at & 31) == 0) {
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                     : "l"(p)
+                     : "memory");
+    } else if (count == 16 && (at & 15) == 0) {
+        const uint4 x = reinterpret_cast<const uint4*>(p)[0], y = reinterpret_cast<const uint4*>(p)[1];
+        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+        w[4] = y.x; w[5] = y.y; w[6] = y.z; w[7] = y.w;
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = j < count ? bf16_to_float(p[j]) : 0.f;
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t lo = 2 * j < count ? p[2 * j] : 0u, hi = 2 * j + 1 < count ? p[2 * j + 1] : 0u;
+            w[j] = lo | hi << 16;
+        }
     }
 }
 
-// Eight consecutive outputs of token t from column n on: v their sums (gated:
-// of the gate, u of the up matrix).
+// Sixteen consecutive outputs of token t from column n on (a multiple of 16): v
+// their sums (gated: of the gate, u of the up matrix), r the residual's words.
 template <int MODE>
-__device__ __forceinline__ void emit8(const Args& a, int t, int n, float (&v)[8], const float (&u)[8]) {
-    const int count = min(8, a.N - n);
+__device__ __forceinline__ void load_residual(const Args& a, int t, int n, uint32_t (&r)[8]) {
+    if constexpr (MODE == kLinear) {
+        if (a.residual != nullptr && t < a.n_tok && n < a.N)
+            load16(a.residual + t * a.ldr + n, r, min(16, a.N - n));
+    }
+}
+template <int MODE>
+__device__ __forceinline__ void emit16(const Args& a, int t, int n, float (&v)[16], const float (&u)[16],
+                                       const uint32_t (&r)[8]) {
+    const int count = min(16, a.N - n);
     if (count <= 0) return;
     if constexpr (MODE == kLinear) {
         if (a.bias != nullptr) {
+            if (count == 16 && (reinterpret_cast<uintptr_t>(a.bias) & 15) == 0) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < count) v[j] += __ldg(a.bias + n + j);
-        }
-        if (a.pre[0] != nullptr) store8(a.pre[0] + t * a.ldpre[0] + n, v, count);
-        if (a.act != GPTQ_ACT_NONE) {
+                for (int j = 0; j < 4; ++j) {
+                    const float4 b = __ldg(reinterpret_cast<const float4*>(a.bias + n) + j);
+                    v[4 * j] += b.x; v[4 * j + 1] += b.y; v[4 * j + 2] += b.z; v[4 * j + 3] += b.w;
+                }
+            } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = activate(v[j], a.act);
+                for (int j = 0; j < 16; ++j)
+                    if (j < count) v[j] += __ldg(a.bias + n + j);
+            }
         }
+        if (a.pre[0] != nullptr) store16(a.pre[0] + t * a.ldpre[0] + n, v, count);
+        activate_all(v, a.act);
         if (a.residual != nullptr) {
-            float r[8];
-            load8(a.residual + t * a.ldr + n, r, count);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] += r[j];
+            for (int j = 0; j < 8; ++j) {
+                v[2 * j] += __uint_as_float(r[j] << 16);
+                v[2 * j + 1] += __uint_as_float(r[j] & 0xFFFF0000u);
+            }
         }
     } else if constexpr (MODE == kGated) {
-        if (a.pre[0] != nullptr) store8(a.pre[0] + t * a.ldpre[0] + n, v, count);
-        if (a.pre[1] != nullptr) store8(a.pre[1] + t * a.ldpre[1] + n, u, count);
+        if (a.pre[0] != nullptr) store16(a.pre[0] + t * a.ldpre[0] + n, v, count);
+        if (a.pre[1] != nullptr) store16(a.pre[1] + t * a.ldpre[1] + n, u, count);
+        activate_all(v, a.act);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = activate(v[j], a.act) * u[j];
+        for (int j = 0; j < 16; ++j) v[j] *= u[j];
     }
-    store8(a.Y + t * a.ldy + n, v, count);
+    store16(a.Y + t * a.ldy + n, v, count);
 }
 
 // ------------------------------------------------------- dequantization
-// The 64 packed codes of a thread's stage as words.
-template <int BITS>
-__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[2 * BITS]) {
+// The NW words (32 or 64 codes) of a thread's stage; 3-bit rows lie on 8-byte
+// boundaries (4-byte for 32 codes), the others on whole vectors.
+template <int BITS, int NW>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[NW]) {
     if constexpr (BITS == 3) {
 #pragma unroll
-        for (int q = 0; q < 3; ++q) {
-            const uint2 v = reinterpret_cast<const uint2*>(p)[q];
-            w[2 * q] = v.x;
-            w[2 * q + 1] = v.y;
-        }
+        for (int q = 0; q < NW; ++q) w[q] = reinterpret_cast<const uint32_t*>(p)[q];
+    } else if constexpr (NW == 2) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        w[0] = v.x;
+        w[1] = v.y;
     } else {
 #pragma unroll
-        for (int q = 0; q < BITS / 2; ++q) {
+        for (int q = 0; q < NW / 4; ++q) {
             const uint4 v = reinterpret_cast<const uint4*>(p)[q];
             w[4 * q] = v.x; w[4 * q + 1] = v.y; w[4 * q + 2] = v.z; w[4 * q + 3] = v.w;
         }
@@ -213,12 +244,12 @@ struct Group {
     }
 };
 
-// Codes 8c .. 8c+7 of a thread's 64 as four bf16x2 weights: per 8 codes 8 masks
+// Codes 8c .. 8c+7 of a thread's words as four bf16x2 weights: per 8 codes 8 masks
 // and a shift, 4 packings and 8 packed fp32 operations on the other pipe (a
 // table look-up by byte permutes takes 23 on the first, which runs 64 lanes per
 // cycle and bound the sweep).
-template <int BITS>
-__device__ __forceinline__ void weights8(const uint32_t (&w)[2 * BITS], int c, const Group<BITS>& g, uint32_t (&o)[4]) {
+template <int BITS, int NW>
+__device__ __forceinline__ void weights8(const uint32_t (&w)[NW], int c, const Group<BITS>& g, uint32_t (&o)[4]) {
     constexpr uint32_t kMagic = 0x4B000000u;
     uint64_t f[4];
     if constexpr (BITS == 8) {
@@ -236,7 +267,7 @@ __device__ __forceinline__ void weights8(const uint32_t (&w)[2 * BITS], int c, c
             v = (c & 1) ? w[c >> 1] >> 16 : w[c >> 1];
         } else {
             const int b = (24 * c) >> 5, sh = (24 * c) & 31;
-            v = sh <= 8 ? (w[b] >> sh) : __funnelshift_r(w[b], w[b + 1 < 6 ? b + 1 : 5], sh);
+            v = sh <= 8 ? (w[b] >> sh) : __funnelshift_r(w[b], w[b + 1 < NW ? b + 1 : NW - 1], sh);
         }
         const uint32_t u = v >> (4 * BITS);
         constexpr uint32_t kMask = (1u << BITS) - 1u;
@@ -259,39 +290,35 @@ __device__ __forceinline__ void weights8(const uint32_t (&w)[2 * BITS], int c, c
 
 // A CTA's accumulators (tokens t0 .. and t0 + step .. in the two halves) through
 // the epilogue, or into partial tile `slot` (whose rows start `row0` before t0).
-// Four warps share a lane quarter's chunks of 32 columns.
+// Four warps share a lane quarter's chunks of 16 columns.
 template <int MODE>
 __device__ __forceinline__ void drain_tile(const Args& a, uint32_t tmem, int slot, int halves, int t0, int step,
                                            int n0, int warp, int lane, int row0) {
     const int q = warp & 3;           // tensor-memory lane quarter of this warp
     const int side = (warp - 3) >> 2;
-    const int chunks = MODE == kGated && slot < 0 ? TN / 64 : TN / 32;
+    const int chunks = MODE == kGated && slot < 0 ? TN / 32 : TN / 16;
 #pragma unroll 1
     for (int e = side; e < halves * chunks; e += kDeqWarps / 4) {
         const int h = e / chunks, c = e % chunks;
         const int t = t0 + h * step + 32 * q + lane;
-        const uint32_t at = tmem + (static_cast<uint32_t>(32 * q) << 16) + h * TN + c * 32;
-        float v[32], u[32];
-        tmem_ld32(at, v);
+        const uint32_t at = tmem + (static_cast<uint32_t>(32 * q) << 16) + h * TN + c * 16;
+        float v[16], u[16];
+        uint32_t r[8];
+        if (slot < 0) load_residual<MODE>(a, t, n0 + c * 16, r);
+        tmem_ld16(at, v);
         if constexpr (MODE == kGated) {
-            if (slot < 0) tmem_ld32(at + TN / 2, u);
+            if (slot < 0) tmem_ld16(at + TN / 2, u);
         }
         if (t < a.n_tok && slot >= 0) {
-            float* p = a.part + (static_cast<int64_t>(slot) * a.part_rows + (t - t0 + row0)) * TN + c * 32;
+            float* p = a.part + (static_cast<int64_t>(slot) * a.part_rows + (t - t0 + row0)) * TN + c * 16;
 #pragma unroll
-            for (int x = 0; x < 8; ++x)
-                reinterpret_cast<float4*>(p)[x] = make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+            for (int x = 0; x < 2; ++x)   // 32 bytes each (the workspace is 256-byte aligned)
+                asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p + 8 * x),
+                             "f"(v[8 * x]), "f"(v[8 * x + 1]), "f"(v[8 * x + 2]), "f"(v[8 * x + 3]), "f"(v[8 * x + 4]),
+                             "f"(v[8 * x + 5]), "f"(v[8 * x + 6]), "f"(v[8 * x + 7])
+                             : "memory");
         } else if (t < a.n_tok) {
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                float vv[8], uu[8];
-#pragma unroll
-                for (int y = 0; y < 8; ++y) {
-                    vv[y] = v[8 * x + y];
-                    uu[y] = MODE == kGated ? u[8 * x + y] : 0.f;
-                }
-                emit8<MODE>(a, t, n0 + c * 32 + 8 * x, vv, uu);
-            }
+            emit16<MODE>(a, t, n0 + c * 16, v, u, r);
         }
         __syncwarp();
     }
@@ -563,17 +590,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 // CTAs the weight tile is dequantized, written and read once instead of twice:
 // 120 KB of shared memory traffic per CTA and stage instead of 176, at 128 bytes
 // per cycle the difference between 940 and 1375 cycles for 1024 of MMAs.
-// Roles as above, with four teams of four dequantizing warps (one thread per 64
-// codes of one of the CTA's 128 rows).  The teams of both CTAs report a stage to
+// Roles as above, a dequantizing thread with 32 codes of one of the CTA's 128
+// rows (a hand-over between the CTAs takes longer than one inside a CTA, so a
+// stage's arithmetic has to be short: four teams of four warps, 64 codes each,
+// took 0.73 us per stage of 256 tokens).  The teams of both CTAs report a stage to
 // rank 0's barrier, and one thread of rank 1 its tokens' arrival.  A thread
 // meets every phase of a barrier that it waits on, in order: a parity wait for
 // phase n returns at once while phase n - 1 is still open.
-constexpr int kTeams = 4;
+constexpr int kTeams = 2;
+constexpr int kTeamWarps = 8;
 constexpr int PM = 512;                       // tokens per pair and tile
 constexpr int kPairBBytes = 128 * BK * 2;     // 16 KB: a CTA's half of the weight tile
-constexpr int kPairAStages = 3;
 constexpr int kHalfBytes = 128 * BK * 2;      // 16 KB: 128 tokens of a stage
-constexpr int kPairABytes = 2 * kHalfBytes;
+constexpr int kPairUnits = 8;                 // of them in the ring: 4 stages of 256 tokens per CTA, 8 of 128
 constexpr uint32_t kPairTmemCols = 512;
 template <int BITS, int MODE>
 struct PairGeom {
@@ -582,15 +611,15 @@ struct PairGeom {
     static constexpr bool kPairs = Geom<BITS, MODE>::kPairs;
     static constexpr int kSlot = Geom<BITS, MODE>::kSlot / 2;
     static constexpr int kPStages = BITS == 8 ? 4 : BITS == 3 && MODE != kBack ? 4 : 8;
-    static constexpr int kBBufs = kTeams;   // a team's own: it meets every phase of its barriers
-    static constexpr int kSmem = kPairAStages * kPairABytes + kBBufs * kPairBBytes + kPStages * kSlot + 1024 + 512;
-    static_assert((kPairs ? 2 * kPStages : kPStages) % kTeams == 0, "rings of whole rounds of the teams");
+    static constexpr int kBBufs = 4;
+    static constexpr int kSmem = kPairUnits * kHalfBytes + kBBufs * kPairBBytes + kPStages * kSlot + 1024 + 512;
+    static_assert((kPairs || kPStages % kTeams == 0) && kBBufs % kTeams == 0, "rings of whole rounds of the teams");
 };
 struct PairBars {
-    uint64_t afull[kPairAStages], aempty[kPairAStages];
-    uint64_t peer[kPairAStages];                // rank 0's: rank 1's tokens have landed
+    uint64_t afull[kPairUnits], aempty[kPairUnits];
+    uint64_t peer[kPairUnits];                  // rank 0's: rank 1's tokens have landed
     uint64_t pfull[8], pempty[8];
-    uint64_t ready[kTeams], bempty[kTeams];     // ready: rank 0's, arrivals of both CTAs
+    uint64_t ready[4], bempty[4];               // ready: rank 0's, arrivals of both CTAs
     uint64_t acc_full, drain;
     uint32_t tmem;
     int abort;
@@ -605,7 +634,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
-    uint8_t* bbuf = smem + kPairAStages * kPairABytes;
+    uint8_t* bbuf = smem + kPairUnits * kHalfBytes;
     uint8_t* pbuf = bbuf + G::kBBufs * kPairBBytes;
     PairBars* bars = reinterpret_cast<PairBars*>(pbuf + G::kPStages * G::kSlot);
     volatile int* abort = &bars->abort;
@@ -622,19 +651,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int t0 = (tile / a.tiles_n) * PM + 128 * rank;     // this CTA's tokens: t0 .. and t0 + 256 ..
     const int n0 = (tile % a.tiles_n) * (MODE == kGated ? TN / 2 : TN);
     const int halves = (tile / a.tiles_n) * PM + 256 < a.n_tok ? 2 : 1;
+    const int depth = kPairUnits / halves, abytes = halves * kHalfBytes;   // of the tokens' ring
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kPairAStages; ++s) {
+        for (int s = 0; s < kPairUnits; ++s) {
             mbar_init(&bars->afull[s], 1);
             mbar_init(&bars->aempty[s], 1);
             mbar_init(&bars->peer[s], 1);
         }
         for (int s = 0; s < G::kPStages; ++s) {
             mbar_init(&bars->pfull[s], 1);
-            mbar_init(&bars->pempty[s], G::kPairs ? 8 : 4);
+            mbar_init(&bars->pempty[s], G::kPairs ? 2 * kTeamWarps : kTeamWarps);
         }
         for (int b = 0; b < G::kBBufs; ++b) {
-            mbar_init(&bars->ready[b], 8);
+            mbar_init(&bars->ready[b], 2 * kTeamWarps);
             mbar_init(&bars->bempty[b], 1);
         }
         mbar_init(&bars->acc_full, 1);
@@ -659,20 +689,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             int i = 0;
             for (int it = k0; it < k1 && !*abort; ++it, ++i) {
-                const int st = i % kPairAStages;
-                if (!mbar_wait_short(&bars->aempty[st], ((i / kPairAStages) & 1u) ^ 1u, abort)) break;
+                const int st = i % depth;
+                if (!mbar_wait_short(&bars->aempty[st], ((i / depth) & 1u) ^ 1u, abort)) break;
                 const bool second = MODE == kBack && it >= a.nk1;
                 const CUtensorMap* map = second ? &tma1 : &tma0;
                 const int x = (second ? it - a.nk1 : it) * BK;
                 mbar_arrive_expect_tx(&bars->afull[st], halves * kHalfBytes);
                 for (int h = 0; h < halves; ++h)
-                    tma_load_2d(smem + st * kPairABytes + h * kHalfBytes, map, &bars->afull[st], x, t0 + 256 * h);
+                    tma_load_2d(smem + st * abytes + h * kHalfBytes, map, &bars->afull[st], x, t0 + 256 * h);
             }
             // never leave with copies in flight (bounded even when aborting)
             volatile int no_abort = 0;
-            for (int j = 0; j < min(i, kPairAStages); ++j) {
+            for (int j = 0; j < min(i, depth); ++j) {
                 const int i2 = i - 1 - j;
-                if (!mbar_wait_short(&bars->afull[i2 % kPairAStages], (i2 / kPairAStages) & 1u, &no_abort)) {
+                if (!mbar_wait_short(&bars->afull[i2 % depth], (i2 / depth) & 1u, &no_abort)) {
                     *abort = 1;
                     break;
                 }
@@ -716,15 +746,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             constexpr uint32_t kIdesc = instr_desc(/*bf16*/ 1, /*A K-major*/ 0, /*B*/ MODE == kBack ? 1 : 0, 256, TN);
             bool ok = true;
             for (int i = 0; i < k1 - k0; ++i) {
-                const int st = i % kPairAStages, b = i % G::kBBufs;
-                if (!mbar_wait_short(&bars->afull[st], (i / kPairAStages) & 1u, abort) ||
-                    !mbar_wait_cluster(&bars->peer[st], (i / kPairAStages) & 1u, abort) ||
+                const int st = i % depth, b = i % G::kBBufs;
+                if (!mbar_wait_short(&bars->afull[st], (i / depth) & 1u, abort) ||
+                    !mbar_wait_cluster(&bars->peer[st], (i / depth) & 1u, abort) ||
                     !mbar_wait_cluster(&bars->ready[b], (i / G::kBBufs) & 1u, abort)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t am = smem_u32(smem + st * kPairABytes);
+                const uint32_t am = smem_u32(smem + st * abytes);
                 const uint32_t bm = smem_u32(bbuf + b * kPairBBytes);
                 for (int h = 0; h < halves; ++h)
 #pragma unroll
@@ -746,16 +776,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // rank 1: passes its tokens' arrival on, in order
             bool ok = true;
             for (int i = 0; i < k1 - k0 && ok; ++i) {
-                const int st = i % kPairAStages;
-                ok = mbar_wait_short(&bars->afull[st], (i / kPairAStages) & 1u, abort);
+                const int st = i % depth;
+                ok = mbar_wait_short(&bars->afull[st], (i / depth) & 1u, abort);
                 if (ok) mbar_arrive_cluster(&bars->peer[st], 0);
             }
             // the last arrivals that rank 0's MMAs send here have to land before this CTA leaves
             volatile int no_abort = 0;
             if (!mbar_wait_short(&bars->drain, 0, &no_abort)) *abort = 1;
-            for (int d = 0; ok && d < kPairAStages && d < k1 - k0; ++d) {
+            for (int d = 0; ok && d < depth && d < k1 - k0; ++d) {
                 const int i = k1 - k0 - 1 - d;
-                mbar_wait_short(&bars->aempty[i % kPairAStages], (i / kPairAStages) & 1u, abort);
+                mbar_wait_short(&bars->aempty[i % depth], (i / depth) & 1u, abort);
             }
             for (int d = 0; ok && d < G::kBBufs && d < k1 - k0; ++d) {
                 const int i = k1 - k0 - 1 - d;
@@ -764,20 +794,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     } else {
         // ------------------------------------------------ dequantize
-        const int j = (threadIdx.x - 96) & 127;   // the thread's 128 bytes of the CTA's half of the tile
-        const int team = (threadIdx.x - 96) >> 7;
+        const int j = (threadIdx.x - 96) & 127;          // 128 bytes of the CTA's half of the tile,
+        const int part = ((threadIdx.x - 96) >> 7) & 1;  // and which 32 of their 64 codes
+        const int team = (threadIdx.x - 96) >> 8;
         const int mi = MODE == kGated ? rank : 0;
         const int wrow = n0 + (MODE == kGated ? 0 : 128 * rank) + j;             // forward
         const int kcol = n0 + 128 * rank + 64 * (j >> 6);                        // backward
         const int groups = (a.d_col + a.g - 1) / a.g;
-        float s[GPT] = {}, s_nx[GPT];
-        int z[GPT] = {}, z_nx[GPT];
+        constexpr int TG = GPT == 1 ? 1 : GPT / 2;                               // groups in 32 codes
+        float s[TG] = {}, s_nx[TG];
+        int z[TG] = {}, z_nx[TG];
         const int span = GPT == 1 ? a.g / BK : 1;
         int gi = GPT == 1 && MODE != kBack ? (k0 + team) / span : 0, rem = GPT == 1 && MODE != kBack ? (k0 + team) % span : 0;
-        const int back_group = GPT == 1 ? kcol / a.g : kcol / 64 * GPT;
+        const int back_group = GPT == 1 ? kcol / a.g : kcol / 64 * GPT + part * TG;
         auto fetch = [&](int it) {
 #pragma unroll
-            for (int q = 0; q < GPT; ++q) {
+            for (int q = 0; q < TG; ++q) {
                 int group, row, m;
                 bool in;
                 if constexpr (MODE == kBack) {
@@ -788,7 +820,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 } else {
                     m = mi;
                     row = wrow;
-                    group = GPT == 1 ? gi : it * GPT + q;
+                    group = GPT == 1 ? gi : it * GPT + part * TG + q;
                     in = it < k1 && row < a.d_row && group < groups;
                 }
                 s_nx[q] = 0.f;   // rows and columns past the layer: weights 0
@@ -799,7 +831,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     z_nx[q] = __ldg(a.mat[m].zeros + at);
                 }
             }
-            if constexpr (GPT == 1 && MODE != kBack) {   // the group four stages on
+            if constexpr (GPT == 1 && MODE != kBack) {   // the group of the team's next stage
                 rem += kTeams;
                 while (rem >= span) {
                     rem -= span;
@@ -809,25 +841,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         };
         fetch(k0 + team);
         Group<BITS> grp;
-        uint32_t dst_off[8];
+        uint32_t dst_off[4];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) dst_off[c] = j * 128 + ((c ^ (j & 7)) << 4);
+        for (int c = 0; c < 4; ++c) dst_off[c] = j * 128 + (((4 * part + c) ^ (j & 7)) << 4);
         bool ok = true;
         for (int it = k0 + team, i = team; it < k1; it += kTeams, i += kTeams) {
             const int pi = G::kPairs ? i >> 1 : i;
             const int ps = pi % G::kPStages, b = i % G::kBBufs;
 #pragma unroll
-            for (int q = 0; q < GPT; ++q) {
+            for (int q = 0; q < TG; ++q) {
                 s[q] = s_nx[q];
                 z[q] = z_nx[q];
             }
             fetch(it + kTeams);
-            if constexpr (GPT == 1) grp.set(s[0], static_cast<float>(z[0]));
+            if constexpr (TG == 1) grp.set(s[0], static_cast<float>(z[0]));
             if (!mbar_wait_short(&bars->pfull[ps], (pi / G::kPStages) & 1u, abort)) {
                 ok = false;
                 break;
             }
-            const uint8_t* src = pbuf + ps * G::kSlot;
+            const uint8_t* src = pbuf + ps * G::kSlot + part * (4 * BITS);
             if constexpr (BITS != 3) {
                 src += j * G::kRowBytes;
             } else if constexpr (MODE == kBack) {
@@ -835,7 +867,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             } else {
                 src += j * G::kRowBytes + (i & 1) * (G::kRowBytes / 2);
             }
-            uint32_t w[2 * BITS];
+            uint32_t w[BITS];
             load_words<BITS>(src, w);
             if (!mbar_wait_short(&bars->bempty[b], ((i / G::kBBufs) & 1u) ^ 1u, abort)) {
                 ok = false;
@@ -843,9 +875,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             const uint32_t tile_at = smem_u32(bbuf + b * kPairBBytes);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                if constexpr (GPT > 1) {
-                    if (c % (8 / GPT) == 0) grp.set(s[c / (8 / GPT)], static_cast<float>(z[c / (8 / GPT)]));
+            for (int c = 0; c < 4; ++c) {
+                if constexpr (TG > 1) {
+                    if (c % (4 / TG) == 0) grp.set(s[c / (4 / TG)], static_cast<float>(z[c / (4 / TG)]));
                 }
                 uint32_t o[4];
                 weights8<BITS>(w, c, grp, o);
@@ -874,32 +906,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // The split tiles: their parts added in order, then the epilogue.  One thread
-// per 8 outputs of a token.
+// per 16 outputs of a token.
 template <int MODE>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args a, int split_tiles) {
     constexpr int kOut = MODE == kGated ? TN / 2 : TN;
-    const int64_t per_tile = static_cast<int64_t>(a.part_rows) * (kOut / 8);
+    const int64_t per_tile = static_cast<int64_t>(a.part_rows) * (kOut / 16);
     const int64_t total = per_tile * split_tiles;
     for (int64_t e = blockIdx.x * 256ll + threadIdx.x; e < total; e += gridDim.x * 256ll) {
-        const int i = static_cast<int>(e / per_tile), r = static_cast<int>(e % per_tile);
-        const int row = r / (kOut / 8), c = (r % (kOut / 8)) * 8;
+        const int i = static_cast<int>(e / per_tile), x = static_cast<int>(e % per_tile);
+        const int row = x / (kOut / 16), c = (x % (kOut / 16)) * 16;
         const int tile = a.full + i;
         const int t = (tile / a.tiles_n) * a.tile_tokens + row, n = (tile % a.tiles_n) * kOut + c;
         if (t >= a.n_tok || n >= a.N) continue;
-        float v[8] = {}, u[8] = {};
-        for (int k = 0; k < a.split; ++k) {
-            const float* p = a.part + ((static_cast<int64_t>(i) * a.split + k) * a.part_rows + row) * TN + c;
+        uint32_t r[8];
+        load_residual<MODE>(a, t, n, r);
+        float v[16] = {}, u[16] = {};
+        const float* p = a.part + (static_cast<int64_t>(i) * a.split * a.part_rows + row) * TN + c;
+#pragma unroll 2
+        for (int k = 0; k < a.split; ++k, p += static_cast<int64_t>(a.part_rows) * TN) {
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const float4 q = reinterpret_cast<const float4*>(p)[x];
-                v[4 * x] += q.x; v[4 * x + 1] += q.y; v[4 * x + 2] += q.z; v[4 * x + 3] += q.w;
+            for (int y = 0; y < 4; ++y) {
+                const float4 q = __ldcs(reinterpret_cast<const float4*>(p) + y);
+                v[4 * y] += q.x; v[4 * y + 1] += q.y; v[4 * y + 2] += q.z; v[4 * y + 3] += q.w;
                 if constexpr (MODE == kGated) {
-                    const float4 w = reinterpret_cast<const float4*>(p + TN / 2)[x];
-                    u[4 * x] += w.x; u[4 * x + 1] += w.y; u[4 * x + 2] += w.z; u[4 * x + 3] += w.w;
+                    const float4 w = __ldcs(reinterpret_cast<const float4*>(p + TN / 2) + y);
+                    u[4 * y] += w.x; u[4 * y + 1] += w.y; u[4 * y + 2] += w.z; u[4 * y + 3] += w.w;
                 }
             }
         }
-        emit8<MODE>(a, t, n, v, u);
+        emit16<MODE>(a, t, n, v, u, r);
     }
 }
 
@@ -998,7 +1033,7 @@ gptq_status run(Args a, const CUtensorMap (&ta)[2], const uint32_t* const (&pack
     if (e != cudaSuccess) return GPTQ_ERR_CUDA;
     ++*launches;
     if (rest > 0) {
-        const int64_t work = static_cast<int64_t>(rest) * a.part_rows * ((MODE == kGated ? TN / 2 : TN) / 8);
+        const int64_t work = static_cast<int64_t>(rest) * a.part_rows * ((MODE == kGated ? TN / 2 : TN) / 16);
         const int64_t want = (work + 255) / 256;
         join_kernel<MODE><<<static_cast<int>(want < 16 * kSms ? want : 16 * kSms), 256, 0, stream>>>(a, rest);
         if (cudaGetLastError() != cudaSuccess) return GPTQ_ERR_CUDA;
