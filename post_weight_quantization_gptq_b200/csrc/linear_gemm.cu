@@ -13,12 +13,12 @@
 //   warp 0      TMA: the stage's tokens (128 x 64 bf16, 128-byte swizzle)
 //   warp 2      TMA: the stage's packed words, in a ring of their own
 //   warp 1      tensor memory and the MMAs (kind::f16, M 128, N 256, K 16)
-//   warps 3..18 dequantize the stage's 256 x 64 weights into a bf16 tile in
-//               shared memory, one thread per 64 codes of one weight row; two
-//               groups of eight warps take every other stage, so that one
-//               group's hand-over (waits, fence, arrivals: 0.35 us) hides behind
-//               the other's arithmetic.  After the sweep they drain the
-//               accumulators through the epilogue
+//   warps 3..   dequantize the stage's 256 x 64 weights into a bf16 tile in
+//               shared memory, one thread per 64 codes of one weight row; teams
+//               of eight warps take the stages in turn, so that one's hand-over
+//               (waits, fence, arrivals) hides behind another's arithmetic
+//               (three teams 0.66 us per stage of 128 tokens, two 0.77).  After
+//               the sweep they drain the accumulators through the epilogue
 // linear    the tile's columns are 256 weight rows n, the stage 64 of their k:
 //           the weight tile is K-major.
 // gated     the columns are 128 rows of the gate and the same 128 of the up
@@ -53,9 +53,11 @@ constexpr int BK = 64;                        // contraction per stage
 constexpr int kAStages = 4;
 constexpr int kABytes = TM * BK * 2;          // 16 KB: a stage's tokens
 constexpr int kBBytes = TN * BK * 2;          // 32 KB: one dequantized tile
-constexpr int kBBufs = 4;
+constexpr int kTeams = 3;                     // of 8 dequantizing warps, each every third stage
+constexpr int kTeamWarps = 8;
+constexpr int kBBufs = 3;
 constexpr int kMaxPStages = 6;
-constexpr int kDeqWarps = 16;                 // two groups of 8, each every other stage
+constexpr int kDeqWarps = kTeams * kTeamWarps;
 constexpr int kThreads = 32 * (3 + kDeqWarps);
 constexpr uint32_t kTmemCols = 256;
 constexpr int kSms = 148;                     // SMs of the device this library is built for
@@ -72,12 +74,12 @@ struct Geom {
     static constexpr int kRowBytes = kBoxWords * 4;
     static constexpr bool kPairs = BITS == 3 && MODE != kBack;   // a slot serves two stages
     static constexpr int kSlot = MODE == kBack ? 64 * TN * BITS / 8 : TN * kRowBytes;
-    static constexpr int kPStages = BITS == 8 ? 2 : BITS == 2 ? 6 : BITS == 3 && MODE != kBack ? 2 : 4;
+    static constexpr int kPStages = (BITS == 8 || kPairs ? 1 : 2) * kTeams;
     static constexpr int kSmem = kAStages * kABytes + kBBufs * kBBytes + kPStages * kSlot + 1024 + 256;
     // a parity wait is only right for the phase after the last one seen, so a
     // team has to meet every phase of a slot or buffer: stages it shares with
     // the other team come back to it
-    static_assert((kPairs || kPStages % 2 == 0) && kBBufs % 2 == 0, "rings of whole rounds of two teams");
+    static_assert(kPStages % kTeams == 0 && kBBufs % kTeams == 0, "rings of whole rounds of the teams");
 };
 
 struct Bars {
@@ -290,15 +292,15 @@ __device__ __forceinline__ void weights8(const uint32_t (&w)[NW], int c, const G
 
 // A CTA's accumulators (tokens t0 .. and t0 + step .. in the two halves) through
 // the epilogue, or into partial tile `slot` (whose rows start `row0` before t0).
-// Four warps share a lane quarter's chunks of 16 columns.
-template <int MODE>
+// WARPS / 4 warps share a lane quarter's chunks of 16 columns.
+template <int MODE, int WARPS>
 __device__ __forceinline__ void drain_tile(const Args& a, uint32_t tmem, int slot, int halves, int t0, int step,
                                            int n0, int warp, int lane, int row0) {
     const int q = warp & 3;           // tensor-memory lane quarter of this warp
     const int side = (warp - 3) >> 2;
     const int chunks = MODE == kGated && slot < 0 ? TN / 32 : TN / 16;
 #pragma unroll 1
-    for (int e = side; e < halves * chunks; e += kDeqWarps / 4) {
+    for (int e = side; e < halves * chunks; e += WARPS / 4) {
         const int h = e / chunks, c = e % chunks;
         const int t = t0 + h * step + 32 * q + lane;
         const uint32_t at = tmem + (static_cast<uint32_t>(32 * q) << 16) + h * TN + c * 16;
@@ -359,10 +361,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int s = 0; s < G::kPStages; ++s) {
             mbar_init(&bars->pfull[s], 1);
-            mbar_init(&bars->pempty[s], G::kPairs ? kDeqWarps : kDeqWarps / 2);
+            mbar_init(&bars->pempty[s], G::kPairs ? 2 * kTeamWarps : kTeamWarps);
         }
         for (int b = 0; b < kBBufs; ++b) {
-            mbar_init(&bars->bfull[b], kDeqWarps / 2);
+            mbar_init(&bars->bfull[b], kTeamWarps);
             mbar_init(&bars->bempty[b], 1);
         }
         mbar_init(&bars->acc_full, 1);
@@ -509,10 +511,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     z_nx[q] = __ldg(a.mat[m].zeros + at);
                 }
             }
-            if constexpr (GPT == 1 && MODE != kBack) {   // the group two stages on
-                rem += 2;
-                if (rem >= span) { rem -= span; ++gi; }
-                if (rem >= span) { rem -= span; ++gi; }
+            if constexpr (GPT == 1 && MODE != kBack) {   // the group of the team's next stage
+                rem += kTeams;
+                while (rem >= span) {
+                    rem -= span;
+                    ++gi;
+                }
             }
         };
         fetch(k0 + team);
@@ -521,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 8; ++c) dst_off[c] = j * 128 + ((c ^ (j & 7)) << 4);
         bool ok = true;
-        for (int it = k0 + team, i = team; it < k1; it += 2, i += 2) {
+        for (int it = k0 + team, i = team; it < k1; it += kTeams, i += kTeams) {
             const int pi = G::kPairs ? i >> 1 : i;
             const int ps = pi % G::kPStages, b = i % kBBufs;
 #pragma unroll
@@ -529,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 s[q] = s_nx[q];
                 z[q] = z_nx[q];
             }
-            fetch(it + 2);
+            fetch(it + kTeams);
             if constexpr (GPT == 1) grp.set(s[0], static_cast<float>(z[0]));
             if (!mbar_wait_short(&bars->pfull[ps], (pi / G::kPStages) & 1u, abort)) {
                 ok = false;
@@ -571,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------ drain: tensor memory -> output
         if (ok && mbar_wait_short(&bars->acc_full, 0, abort)) {
             tc_fence_after();
-            drain_tile<MODE>(a, tmem, slot, 1, t0, 0, n0, warp, lane, 0);
+            drain_tile<MODE, kDeqWarps>(a, tmem, slot, 1, t0, 0, n0, warp, lane, 0);
         }
     }
 
@@ -597,11 +601,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 // rank 0's barrier, and one thread of rank 1 its tokens' arrival.  A thread
 // meets every phase of a barrier that it waits on, in order: a parity wait for
 // phase n returns at once while phase n - 1 is still open.
-constexpr int kTeams = 2;
-constexpr int kTeamWarps = 8;
 constexpr int PM = 512;                       // tokens per pair and tile
 constexpr int kPairBBytes = 128 * BK * 2;     // 16 KB: a CTA's half of the weight tile
 constexpr int kHalfBytes = 128 * BK * 2;      // 16 KB: 128 tokens of a stage
+constexpr int kPairTeams = 2;                 // of 8 warps (three gained nothing)
+constexpr int kPairDeqWarps = kPairTeams * kTeamWarps;
+constexpr int kPairThreads = 32 * (3 + kPairDeqWarps);
+constexpr int kPairBBufs = 4;
 constexpr int kPairUnits = 8;                 // of them in the ring: 4 stages of 256 tokens per CTA, 8 of 128
 constexpr uint32_t kPairTmemCols = 512;
 template <int BITS, int MODE>
@@ -610,23 +616,23 @@ struct PairGeom {
     static constexpr int kRowBytes = Geom<BITS, MODE>::kRowBytes;
     static constexpr bool kPairs = Geom<BITS, MODE>::kPairs;
     static constexpr int kSlot = Geom<BITS, MODE>::kSlot / 2;
-    static constexpr int kPStages = BITS == 8 ? 4 : BITS == 3 && MODE != kBack ? 4 : 8;
-    static constexpr int kBBufs = 4;
+    static constexpr int kPStages = BITS == 8 || kPairs ? 4 : 8;
+    static constexpr int kBBufs = kPairBBufs;
     static constexpr int kSmem = kPairUnits * kHalfBytes + kBBufs * kPairBBytes + kPStages * kSlot + 1024 + 512;
-    static_assert((kPairs || kPStages % kTeams == 0) && kBBufs % kTeams == 0, "rings of whole rounds of the teams");
+    static_assert(kPStages % kPairTeams == 0 && kBBufs % kPairTeams == 0, "rings of whole rounds of the teams");
 };
 struct PairBars {
     uint64_t afull[kPairUnits], aempty[kPairUnits];
     uint64_t peer[kPairUnits];                  // rank 0's: rank 1's tokens have landed
     uint64_t pfull[8], pempty[8];
-    uint64_t ready[4], bempty[4];               // ready: rank 0's, arrivals of both CTAs
+    uint64_t ready[kPairBBufs], bempty[kPairBBufs];               // ready: rank 0's, arrivals of both CTAs
     uint64_t acc_full, drain;
     uint32_t tmem;
     int abort;
 };
 
 template <int BITS, int GPT, int MODE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     pair_gemm_kernel(const __grid_constant__ CUtensorMap tma0, const __grid_constant__ CUtensorMap tma1,
                      const __grid_constant__ CUtensorMap tmp0, const __grid_constant__ CUtensorMap tmp1,
                      const __grid_constant__ Args a) {
@@ -832,7 +838,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             }
             if constexpr (GPT == 1 && MODE != kBack) {   // the group of the team's next stage
-                rem += kTeams;
+                rem += kPairTeams;
                 while (rem >= span) {
                     rem -= span;
                     ++gi;
@@ -845,7 +851,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) dst_off[c] = j * 128 + (((4 * part + c) ^ (j & 7)) << 4);
         bool ok = true;
-        for (int it = k0 + team, i = team; it < k1; it += kTeams, i += kTeams) {
+        for (int it = k0 + team, i = team; it < k1; it += kPairTeams, i += kPairTeams) {
             const int pi = G::kPairs ? i >> 1 : i;
             const int ps = pi % G::kPStages, b = i % G::kBBufs;
 #pragma unroll
@@ -853,7 +859,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 s[q] = s_nx[q];
                 z[q] = z_nx[q];
             }
-            fetch(it + kTeams);
+            fetch(it + kPairTeams);
             if constexpr (TG == 1) grp.set(s[0], static_cast<float>(z[0]));
             if (!mbar_wait_short(&bars->pfull[ps], (pi / G::kPStages) & 1u, abort)) {
                 ok = false;
@@ -893,7 +899,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // ------------------------------------------------ drain: tensor memory -> output
         if (ok && mbar_wait_short(&bars->acc_full, 0, abort)) {
             tc_fence_after();
-            drain_tile<MODE>(a, tmem, slot, halves, t0, 256, n0, warp, lane, 128 * rank);
+            drain_tile<MODE, kPairDeqWarps>(a, tmem, slot, halves, t0, 256, n0, warp, lane, 128 * rank);
         }
     }
 
@@ -946,9 +952,10 @@ struct Plan {
     size_t part_bytes;
 };
 
-// Pairs of CTAs from here on: below, half of a pair's 256 token rows would be
-// empty, and single CTAs with one half tile spread the weights over more SMs.
-constexpr int kPairTokens = 129;
+// Pairs of CTAs from here on.  A pair's stage of 512 tokens takes 0.93 us on two
+// SMs, one of up to 256 tokens still 0.8; a single CTA's of 128 takes 0.66, so
+// two of those serve 256 tokens better.
+constexpr int kPairTokens = 257;
 
 Plan make_plan(int64_t n_tok, int64_t N, int nk, bool gated, bool pairs) {
     Plan p;
@@ -992,7 +999,7 @@ cudaError_t launch_one(const CUtensorMap (&ta)[2], const CUtensorMap (&tp)[2], c
                   "shared memory per CTA");
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kern<<<pair ? 2 * units : units, kThreads, smem, stream>>>(ta[0], ta[1], tp[0], tp[1], a);
+    kern<<<pair ? 2 * units : units, pair ? kPairThreads : kThreads, smem, stream>>>(ta[0], ta[1], tp[0], tp[1], a);
     return cudaGetLastError();
 }
 
