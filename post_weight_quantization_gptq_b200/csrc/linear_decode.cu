@@ -69,6 +69,7 @@ struct Args {
     int gathered;            // the tokens are written by the kernel launched just before
     int depth;               // blocks of the ring
     int slot_bytes;          // of one: weights, then tokens
+    int red_at;              // where the partial sums lie in shared memory, after the rings
     int ngb_log2;            // groups per block (kNarrow, kTiny)
     int blocks_per_group;    // (kWide)
     uint32_t group_magic;    // block / blocks_per_group = high word of block * group_magic; 0: divide
@@ -194,7 +195,6 @@ struct Shape {
     static constexpr int kRowBytes = 16 * BITS;              // 128 codes
     static constexpr int kWBytes = kRows * kRowBytes;        // of a block
     static constexpr int kPitch = kRows + 4;                 // of the partial sums
-    static constexpr int kRedBytes = kWarps * 8 * NT * kPitch * 4;
     static constexpr int kHead = 1024;                       // barriers
 };
 
@@ -204,7 +204,6 @@ __global__ void __launch_bounds__(kThreads, NT * MT >= 8 ? 1 : 2)
                   const __grid_constant__ CUtensorMap tmx, const __grid_constant__ Args a) {
     using S = Shape<BITS, NT, MT>;
     constexpr int kRows = S::kRows;
-    constexpr int kTok = 8 * NT;
     constexpr int kTilesM = GATED ? MT / 2 : MT;             // tiles of one matrix
     constexpr int kOut = 16 * kTilesM;                       // outputs of the CTA
     extern __shared__ __align__(1024) uint8_t sm[];
@@ -214,11 +213,13 @@ __global__ void __launch_bounds__(kThreads, NT * MT >= 8 ? 1 : 2)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g8 = lane >> 2, t = lane & 3;
-    const int n0 = blockIdx.x * kOut;
     const int ranks = gridDim.y, rank = blockIdx.y;
     const int nblk = (a.K + kBlock - 1) / kBlock;
     const int first = rank * kWarps + warp, stride = ranks * kWarps;
-    const int steps = nblk > first ? (nblk - first + stride - 1) / stride : 0;   // blocks of this warp
+    const int steps = nblk > first ? (nblk - first + stride - 1) / stride : 0;   // blocks of this warp, per tile
+    const int tiles = (a.N + kOut - 1) / kOut;               // the CTA's: blockIdx.x, + gridDim.x, ...
+    const int mine = (tiles - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+    const int items = mine * steps;                          // blocks of this warp in all
     const int depth = a.depth;
     const int ngb_log2 = MODE == kWide ? 0 : a.ngb_log2;     // groups per block
     const int groups = (a.K + a.g - 1) / a.g;
@@ -229,8 +230,11 @@ __global__ void __launch_bounds__(kThreads, NT * MT >= 8 ? 1 : 2)
     const int sc_bytes = 2 * kRows * 4 << ngb_log2;          // a block's scales, then zero points
     uint8_t* sc_ring = sm + S::kHead + kWarps * depth * a.slot_bytes + warp * depth * sc_bytes;
 
+    // The ring runs on through the CTA's tiles: (next_s, next_n0) is the block to
+    // load next, of the tile of outputs from next_n0 on.
+    int next_s = 0, next_n0 = blockIdx.x * kOut;
     // lane 0: a block's weights, and its tokens
-    auto load_weights = [&](int s, int slot) {
+    auto load_weights = [&](int s, int n0, int slot) {
         const int x = (first + s * stride) * (4 * BITS);
         const uint32_t dst = ring + slot * a.slot_bytes;
         mbar_arrive_expect_tx(&full[slot], S::kWBytes + 2 * half_bytes);
@@ -252,29 +256,28 @@ __global__ void __launch_bounds__(kThreads, NT * MT >= 8 ? 1 : 2)
     constexpr int kOwn = (kRows + 31) / 32;                  // rows per lane
     const float* sc_src[kOwn];
     int64_t z_off[kOwn];                                     // bytes from there to the zero point
-    bool live[kOwn];
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) {
-        const int r = lane + 32 * i, n = n0 + r % kOut;
+        const int r = lane + 32 * i;
         const PackedMatrix& m = a.mat[GATED && r >= kOut ? 1 : 0];
-        live[i] = r < kRows && n < a.N;
-        sc_src[i] = m.scales + (live[i] ? n : 0);
+        sc_src[i] = m.scales + r % kOut;
         z_off[i] = reinterpret_cast<const char*>(m.zeros) - reinterpret_cast<const char*>(m.scales);
     }
-    auto load_scales = [&](int b, int slot) {
+    auto load_scales = [&](int s, int n0, int slot) {
+        const int b = first + s * stride;
         const uint32_t dst = smem_u32(sc_ring) + slot * sc_bytes + 4 * lane;
         for (int q = 0; q < (1 << ngb_log2); ++q) {
             // kWide: block / blocks per group, as a multiplication where that is exact
             const int gi = MODE != kWide ? (b << ngb_log2) + q
                          : a.group_magic != 0 ? static_cast<int>(__umulhi(b, a.group_magic)) : b / a.blocks_per_group;
-            const int64_t off = static_cast<int64_t>(gi) * a.N;
+            const int64_t off = static_cast<int64_t>(gi) * a.N + n0;
 #pragma unroll
             for (int i = 0; i < kOwn; ++i) {
-                const bool in = live[i] && gi < groups;
-                const char* src = reinterpret_cast<const char*>(sc_src[i] + (in ? off : 0));
+                const bool in = n0 + (lane + 32 * i) % kOut < a.N && gi < groups;
+                const char* src = reinterpret_cast<const char*>(in ? sc_src[i] + off : a.mat[0].scales);
                 if (kRows % 32 == 0 || lane + 32 * i < kRows) {
                     cp4(dst + 4 * (q * kRows + 32 * i), src, in);
-                    cp4(dst + 4 * (q * kRows + 32 * i) + sc_bytes / 2, src + z_off[i], in);
+                    cp4(dst + 4 * (q * kRows + 32 * i) + sc_bytes / 2, in ? src + z_off[i] : src, in);
                 }
             }
         }
@@ -289,30 +292,34 @@ __global__ void __launch_bounds__(kThreads, NT * MT >= 8 ? 1 : 2)
             tma_prefetch_desc(&tmw0);
             tma_prefetch_desc(&tmx);
         }
-        // a warp's barriers are its own: its copies need not wait for the others
-        for (int d = 0; d < depth && d < steps; ++d) {
-            load_weights(d, d);
-            if (!a.gathered) load_tokens(d, d);
-        }
     }
+    // a warp's barriers are its own: its copies need not wait for the others
+    auto advance = [&]() {
+        if (++next_s == steps) {
+            next_s = 0;
+            next_n0 += gridDim.x * kOut;
+        }
+    };
+    const int ahead = min(depth, items);
     for (int d = 0; d < depth; ++d) {
-        if (d < steps) load_scales(first + d * stride, d);
+        if (d < ahead) {
+            if (lane == 0) {
+                load_weights(next_s, next_n0, d);
+                if (!a.gathered) load_tokens(next_s, d);
+            }
+            load_scales(next_s, next_n0, d);
+            advance();
+        }
         cp_commit();
     }
     if (a.gathered) {
         pdl_wait();   // the tokens come from the kernel before; weights and scales do not
         if (lane == 0)
-            for (int d = 0; d < depth && d < steps; ++d) load_tokens(d, d);
+            for (int d = 0; d < ahead; ++d) load_tokens(d % steps, d);
     }
     __syncthreads();   // the abort word is set up
 
     float acc[MT][NT][4];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int q = 0; q < NT; ++q)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[m][q][i] = 0.f;
 
     // Where a lane reads in a slot (slots lie on 1024-byte boundaries).  Column
     // g8 of a token tile stands for token (g8 >> 1) | (g8 & 1) << 2, so that
@@ -334,11 +341,20 @@ __global__ void __launch_bounds__(kThreads, NT * MT >= 8 ? 1 : 2)
     int slot = 0;
     uint32_t phase = 0;
     bool ok = true;
-    int done = 0;
-    for (int s = 0; s < steps; ++s) {
-        if (!mbar_wait(&full[slot], phase, abort)) {
+    int done = 0;   // blocks consumed
+    float* red = reinterpret_cast<float*>(sm + a.red_at);    // [kWarps][n_tok][kPitch]
+    cg::cluster_group cluster = cg::this_cluster();
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const int n0 = tile * kOut;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int q = 0; q < NT; ++q)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[m][q][i] = 0.f;
+    for (int s = 0; s < steps && ok; ++s, ++done) {
+        if (!mbar_wait_short(&full[slot], phase, abort)) {
             ok = false;
-            done = s;
             break;
         }
         cp_wait(depth - 1);
@@ -448,12 +464,13 @@ __global__ void __launch_bounds__(kThreads, NT * MT >= 8 ? 1 : 2)
             }
         }
         __syncwarp();   // every lane has read the slot
-        if (s + depth < steps) {
+        if (done + depth < items) {
             if (lane == 0) {
-                load_weights(s + depth, slot);
-                load_tokens(s + depth, slot);
+                load_weights(next_s, next_n0, slot);
+                load_tokens(next_s, slot);
             }
-            load_scales(b + depth * stride, slot);
+            load_scales(next_s, next_n0, slot);
+            advance();
         }
         cp_commit();
         if (++slot == depth) {
@@ -461,48 +478,46 @@ __global__ void __launch_bounds__(kThreads, NT * MT >= 8 ? 1 : 2)
             phase ^= 1u;
         }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    if (!ok && lane == 0) {
-        // never leave with copies in flight (bounded): blocks `done` on, as far
-        // as they were issued
-        volatile int no_abort = 0;
-        for (int s = done; s < steps && s < done + depth; ++s)
-            if (!mbar_wait(&full[s % depth], (s / depth) & 1u, &no_abort)) break;
-    }
-
-    // ---- partial sums of the K slices: within the CTA, then the cluster
-    __syncthreads();   // the rings are free
-    float* red = reinterpret_cast<float*>(sm + S::kHead);   // [kWarps][kTok][kPitch]
+    // ---- partial sums of the K slices: within the CTA, then the cluster (whose
+    // CTAs have one tile each)
+    if (a.red_at == S::kHead) __syncthreads();   // the sums take the place of the rings
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int q = 0; q < NT; ++q)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int col = 2 * t + (i & 1);   // its token, as above
-                red[(warp * kTok + 8 * q + ((col >> 1) | (col & 1) << 2)) * S::kPitch + m * 16 + g8 + 8 * (i >> 1)] =
-                    acc[m][q][i];
+                const int col = 2 * t + (i & 1), tk = 8 * q + ((col >> 1) | (col & 1) << 2);   // its token, as above
+                if (tk < a.n_tok) red[(warp * a.n_tok + tk) * S::kPitch + m * 16 + g8 + 8 * (i >> 1)] = acc[m][q][i];
             }
     __syncthreads();
-    for (int e = threadIdx.x; e < kTok * kRows; e += kThreads) {
-        const int tk = e / kRows, r = e % kRows;
-        if (tk >= a.n_tok) break;
-        float v = red[tk * S::kPitch + r];
+    if (ranks > 1) {
+        for (int e = threadIdx.x; e < a.n_tok * kRows; e += kThreads) {
+            const int tk = e / kRows, r = e % kRows;
+            float v = red[tk * S::kPitch + r];
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) v += red[(w * kTok + tk) * S::kPitch + r];
-        red[tk * S::kPitch + r] = v;   // each entry has one owner
+            for (int w = 1; w < kWarps; ++w) v += red[(w * a.n_tok + tk) * S::kPitch + r];
+            red[tk * S::kPitch + r] = v;   // each entry has one owner
+        }
+        cluster.sync();
     }
-    cg::cluster_group cluster = cg::this_cluster();
-    if (ranks > 1) cluster.sync(); else __syncthreads();
     for (int e = rank * kThreads + threadIdx.x; e < a.n_tok * kOut; e += ranks * kThreads) {
         const int tk = e / kOut, r = e % kOut, n = n0 + r;
         if (n >= a.N) continue;
         float v = 0.f, u = 0.f;
-        for (int k = 0; k < ranks; ++k) {
-            float* p = red + tk * S::kPitch + r;
-            if (ranks > 1) p = cluster.map_shared_rank(p, k);
-            v += p[0];
-            if constexpr (GATED) u += p[kOut];
+        if (ranks > 1) {
+            for (int k = 0; k < ranks; ++k) {
+                const float* p = cluster.map_shared_rank(red + tk * S::kPitch + r, k);
+                v += p[0];
+                if constexpr (GATED) u += p[kOut];
+            }
+        } else {
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float* p = red + (w * a.n_tok + tk) * S::kPitch + r;
+                v += p[0];
+                if constexpr (GATED) u += p[kOut];
+            }
         }
         v *= kScaleBack;
         float y;
@@ -516,6 +531,16 @@ __global__ void __launch_bounds__(kThreads, NT * MT >= 8 ? 1 : 2)
         a.Y[tk * a.ldy + n] = f32_to_bf16_bits(y);
     }
     if (ranks > 1) cluster.sync();   // no CTA leaves while its sums are read
+    else if (tile + static_cast<int>(gridDim.x) < tiles) __syncthreads();   // the sums are rewritten
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (!ok && lane == 0) {
+        // never leave with copies in flight (bounded): blocks `done` on, as far
+        // as they were issued
+        volatile int no_abort = 0;
+        for (int i = done; i < items && i < done + depth; ++i)
+            if (!mbar_wait(&full[i % depth], (i / depth) & 1u, &no_abort)) break;
+    }
     if (threadIdx.x == 0 && *abort) report(a.status, GPTQ_ERR_TIMEOUT);
 }
 
@@ -560,7 +585,7 @@ cudaError_t launch_one(Args a, const Launch& l) {
     // split K over a cluster while all CTAs still run in one wave (two per SM) and
     // every warp keeps at least two blocks
     int ranks = 1;
-    while (ranks < 8 && 2 * tiles * ranks <= 2 * num_sms() && nblk >= 4 * ranks * kWarps) ranks *= 2;
+    while (ranks < 8 && tiles * ranks <= num_sms() && nblk >= 4 * ranks * kWarps) ranks *= 2;
     const int steps = (nblk + kWarps * ranks - 1) / (kWarps * ranks);
     const int ngb = MODE == kWide ? 1 : kBlock / a.g;
     for (a.ngb_log2 = 0; (1 << a.ngb_log2) < ngb; ++a.ngb_log2) {}
@@ -573,11 +598,23 @@ cudaError_t launch_one(Args a, const Launch& l) {
                         ? static_cast<uint32_t>(magic) : 0;
     a.slot_bytes = (S::kWBytes + a.n_tok * 256 + 1023) / 1024 * 1024;
     const int per = kWarps * (a.slot_bytes + S::kRows * 8 * ngb);
-    int room = ((NT * MT >= 8 ? kSmemOne : kSmemTwo) - S::kHead) / per;
-    if (room < 2) room = (kSmemOne - S::kHead) / per;
-    a.depth = room < 1 ? 1 : room > kMaxDepth ? kMaxDepth : room;
-    if (a.depth > steps) a.depth = steps;
-    const int smem = S::kHead + (a.depth * per > S::kRedBytes ? a.depth * per : S::kRedBytes);
+    const int sums = kWarps * a.n_tok * S::kPitch * 4;       // the warps' partial sums
+    const int per_sm = NT * MT >= 8 ? 1 : 2, room = (per_sm == 1 ? kSmemOne : kSmemTwo) - S::kHead;
+    // More tiles than CTAs run at a time: these go through the tiles in turn, their
+    // rings running on, if the partial sums leave the rings two blocks (2 x
+    // 11008 x 4096 at one token 17.6 against 19.4 us).  Otherwise the sums take
+    // the rings' place after a CTA's only tile.
+    const int wave = per_sm * num_sms();
+    const bool turns = tiles > wave && room - sums >= 2 * per;
+    const int grid = turns ? wave : tiles;
+    const int items = steps * (turns ? (tiles + wave - 1) / wave : 1);
+    int depth = (turns ? room - sums : room) / per;
+    if (depth < 2) depth = (kSmemOne - S::kHead) / per;      // one CTA per SM then
+    if (depth < 1) return cudaErrorInvalidConfiguration;
+    a.depth = depth > kMaxDepth ? kMaxDepth : depth;
+    if (a.depth > items) a.depth = items;
+    a.red_at = turns ? S::kHead + a.depth * per : S::kHead;
+    const int smem = turns || a.depth * per < sums ? a.red_at + sums : S::kHead + a.depth * per;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     constexpr Swz kSwz = BITS == 8 ? Swz::k128 : BITS == 4 ? Swz::k64 : BITS == 2 ? Swz::k32 : Swz::kNone;
@@ -590,7 +627,7 @@ cudaError_t launch_one(Args a, const Launch& l) {
     if (!GATED) tw[1] = tw[0];
     if (!make_tmap_2d(&tx, true, l.X, a.K, a.n_tok, l.ldx, 64, a.n_tok, Swz::k128)) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(tiles, ranks);
+    cfg.gridDim = dim3(grid, ranks);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = l.stream;
