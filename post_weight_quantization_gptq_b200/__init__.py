@@ -444,6 +444,7 @@ def _activation(name) -> int:
 _Tensor = torch.Tensor
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _refuse(t, name: str, dtype, dev: int) -> None:
@@ -456,12 +457,12 @@ def _refuse(t, name: str, dtype, dev: int) -> None:
 
 
 def _first(t, name: str) -> int:
-    """The device index of a call's first operand (bf16), which has to be the
-    current device: the library launches there."""
+    """The device index of a call's first operand (2-D, bf16), which has to be
+    the current device: the library launches there."""
     if not isinstance(t, _Tensor) or t.dtype is not _BF16 or not t.is_cuda:
         _refuse(t, name, _BF16, 0)
     dev = t.get_device()
-    if dev != torch.cuda.current_device():
+    if dev != _current_device():
         raise ValueError(f"{name} is on cuda:{dev} but cuda:{torch.cuda.current_device()} is current: "
                          "make its device current (torch.cuda.device(...))")
     if t.dim() != 2:
@@ -529,16 +530,22 @@ def _status(t, dev: int):
 
 def _layer(packed, scales, zeros, bits: int, group_size: int, d_col: int, dev: int, suffix: str = ""):
     """Addresses of a packed layer of input width d_col, and its d_row."""
-    if not isinstance(packed, _Tensor) or packed.dtype is not _I32 or packed.get_device() != dev:
-        _refuse(packed, "packed" + suffix, _I32, dev)
+    for t, name, dtype in ((packed, "packed", _I32), (scales, "scales", _F32), (zeros, "zeros", _I32)):
+        if not isinstance(t, _Tensor) or t.dtype is not dtype or t.get_device() != dev:
+            _refuse(t, name + suffix, dtype, dev)
+        if not t.is_contiguous():
+            raise ValueError(f"{name}{suffix} must be contiguous")
+    if packed.dim() != 2 or packed.shape[1] != -(-(d_col * bits) // 32):
+        raise ValueError(f"packed{suffix} must be d_row x {-(-(d_col * bits) // 32)} words, "
+                         f"got {tuple(packed.shape)}")
     d_row = packed.shape[0]
-    p = _whole(packed, "packed" + suffix, _I32, (d_row, -(-(d_col * bits) // 32)), dev)
-    if group_size < 1 and group_size != -1:
-        return p, _ptr(scales), _ptr(zeros), d_row   # the library refuses the group size
-    g = d_col if group_size == -1 or group_size > d_col else group_size
-    shape = (-(-d_col // g), d_row)
-    return (p, _whole(scales, "scales" + suffix, _F32, shape, dev),
-            _whole(zeros, "zeros" + suffix, _I32, shape, dev), d_row)
+    if group_size > 0 or group_size == -1:   # (the library refuses the others)
+        g = d_col if group_size == -1 or group_size > d_col else group_size
+        shape = (-(-d_col // g), d_row)
+        if scales.shape != shape or zeros.shape != shape:
+            raise ValueError(f"scales{suffix} and zeros{suffix} must be {shape[0]} x {d_row}, "
+                             f"got {tuple(scales.shape)} and {tuple(zeros.shape)}")
+    return packed.data_ptr(), scales.data_ptr(), zeros.data_ptr(), d_row
 
 
 def gptq_dequant_matmul_linear(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor,

@@ -19,7 +19,7 @@ namespace {
 constexpr int kCols = 256;      // columns per CTA: 32 lanes x 8
 constexpr int kRows = 8;        // token rows in flight per CTA
 constexpr int kMaxSlabs = 256;  // token slabs of the bias sums
-constexpr int kSlab = 16;       // tokens of one, at least
+constexpr int kSlab = 8;        // tokens of one, at least
 
 // Tokens per CTA: kSlab, or as many as leave at most kMaxSlabs slabs.
 int64_t slab_tokens(int64_t n_tok) {
@@ -135,16 +135,23 @@ __global__ void __launch_bounds__(256) slopes_kernel(const __grid_constant__ Bac
     }
 }
 
+// dbias[n] = the slabs' sums: 32 columns per CTA, eight chains of slabs each,
+// joined in a fixed order.
 __global__ void __launch_bounds__(256) bias_sum_kernel(const float* __restrict__ part, int slabs, int64_t d_row,
                                                        float* __restrict__ dbias) {
-    const int64_t n = blockIdx.x * 256ll + threadIdx.x;
-    if (n >= d_row) return;
-    float v[4] = {};   // four chains, joined in a fixed order
-    for (int s = 0; s < slabs; s += 4)
+    __shared__ float sums[8][32];
+    const int col = threadIdx.x & 31, chain = threadIdx.x >> 5;
+    const int64_t n = blockIdx.x * 32ll + col;
+    float v = 0.f;
+    if (n < d_row)
+        for (int s = chain; s < slabs; s += 8) v += part[s * d_row + n];
+    sums[chain][col] = v;
+    __syncthreads();
+    if (chain == 0 && n < d_row) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            if (s + q < slabs) v[q] += part[(s + q) * d_row + n];
-    dbias[n] = (v[0] + v[1]) + (v[2] + v[3]);
+        for (int q = 1; q < 8; ++q) v += sums[q][col];
+        dbias[n] = v;
+    }
 }
 
 constexpr int kScatterThreads = 512;
@@ -220,7 +227,7 @@ gptq_status launch_slopes(const BackwardCall& c, float* bias_part, int64_t* laun
     if (cudaGetLastError() != cudaSuccess) return GPTQ_ERR_CUDA;
     ++*launches;
     if (bias_part != nullptr) {
-        bias_sum_kernel<<<static_cast<unsigned>((c.d_row + 255) / 256), 256, 0, stream>>>(
+        bias_sum_kernel<<<static_cast<unsigned>((c.d_row + 31) / 32), 256, 0, stream>>>(
             bias_part, static_cast<int>(ns), c.d_row, c.dbias);
         if (cudaGetLastError() != cudaSuccess) return GPTQ_ERR_CUDA;
         ++*launches;
