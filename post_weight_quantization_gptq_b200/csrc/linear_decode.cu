@@ -13,8 +13,8 @@
 // fp32's normal range; the result is scaled back at the end.  The sums run on
 // the tensor cores (m16n8k16, 16 weight rows by 8 tokens, exact products,
 // fp32 sums), the plain token sum through one more tile whose codes are all 1,
-// so that it lands in the registers that need it.  Tokens of magnitude 2^63
-// and more overflow; below 2^-57 the products lose relative precision (2^-80
+// so that it lands in the registers that need it.  Tokens of magnitude 2^64
+// and more may overflow; below 2^-57 the products lose relative precision (2^-80
 // absolute).
 //
 // Bound: the packed layer is read once for up to 32 tokens, so HBM; below
