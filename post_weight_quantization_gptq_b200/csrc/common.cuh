@@ -48,6 +48,26 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+// A permutation of K <= 65536 columns (K a multiple of 4) as 16-bit indices in
+// shared memory, by all `threads` of the CTA: entries outside [0, K) become their
+// position.  Eight loads in flight per thread (one at a time, the loop's
+// latency was most of a short gather).
+__device__ __forceinline__ void stage_permutation(uint16_t* idx, const int32_t* perm, int K, int threads) {
+    auto in_range = [K](int col, int k) { return static_cast<uint32_t>(col >= 0 && col < K ? col : k); };
+    if (perm != nullptr && (reinterpret_cast<uintptr_t>(perm) & 15) == 0) {
+#pragma unroll 2
+        for (int k = 4 * threadIdx.x; k < K; k += 4 * threads) {
+            const int4 c = __ldg(reinterpret_cast<const int4*>(perm + k));
+            *reinterpret_cast<uint2*>(idx + k) =
+                make_uint2(in_range(c.x, k) | in_range(c.y, k + 1) << 16, in_range(c.z, k + 2) | in_range(c.w, k + 3) << 16);
+        }
+    } else {
+#pragma unroll 8
+        for (int k = threadIdx.x; k < K; k += threads)
+            idx[k] = static_cast<uint16_t>(perm != nullptr ? in_range(__ldg(perm + k), k) : static_cast<uint32_t>(k));
+    }
+}
+
 // ---------------------------------------------------------------- mbarrier
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count));

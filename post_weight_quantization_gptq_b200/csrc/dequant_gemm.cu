@@ -387,11 +387,6 @@ gather_bf16_piped_kernel(const uint16_t* __restrict__ X, int64_t ldx, int64_t n_
     uint16_t* idx = gs;            // [K] source column of each position
     uint16_t* rows = gs + K;       // [2][K] token rows
     const int chunks = K / 8;
-    for (int k = threadIdx.x; k < K; k += kPipeThreads) {
-        int col = perm != nullptr ? perm[k] : k;
-        if (col < 0 || col >= K) col = k;
-        idx[k] = static_cast<uint16_t>(col);
-    }
     auto fetch = [&](int64_t t, int buf) {
         if (t < n_tok) {
             const uint16_t* xr = X + t * ldx;
@@ -403,6 +398,7 @@ gather_bf16_piped_kernel(const uint16_t* __restrict__ X, int64_t ldx, int64_t n_
     };
     int buf = 0;
     fetch(blockIdx.x, 0);
+    stage_permutation(idx, perm, K, kPipeThreads);
     for (int64_t t = blockIdx.x; t < n_tok; t += gridDim.x) {
         fetch(t + gridDim.x, buf ^ 1);
         cp_async_wait_older();  // this thread's copies of row t have landed
@@ -435,7 +431,13 @@ cudaError_t launch_gather(const uint16_t* X, int64_t ldx, int64_t n_tok, int K,
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(piped));
         if (e != cudaSuccess) return e;
-        const int grid = static_cast<int>(n_tok < num_sms() ? n_tok : num_sms());
+        // as many CTAs as fit: with one per SM a few hundred rows were a chain of
+        // three or four rows each (500 x 11008: 10.3 us)
+        int per_sm = 0;
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kPipeThreads, piped);
+        if (e != cudaSuccess) return e;
+        const int64_t resident = static_cast<int64_t>(per_sm > 0 ? per_sm : 1) * num_sms();
+        const int grid = static_cast<int>(n_tok < resident ? n_tok : resident);
         kern<<<grid, kPipeThreads, piped, stream>>>(X, ldx, n_tok, K, perm, Xq);
         return cudaGetLastError();
     }

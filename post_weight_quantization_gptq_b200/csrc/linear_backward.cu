@@ -176,12 +176,9 @@ __global__ void __launch_bounds__(kScatterThreads) scatter_kernel(const uint16_t
     }
     uint16_t* idx = sm;        // [K]
     uint16_t* row = sm + K;    // [K]
-    for (int k = threadIdx.x; k < K; k += kScatterThreads) {
-        int col = perm[k];
-        if (col < 0 || col >= K) col = k;
-        idx[k] = static_cast<uint16_t>(col);
-        row[k] = 0;
-    }
+    stage_permutation(idx, perm, K, kScatterThreads);
+    for (int k = 8 * threadIdx.x; k < K; k += 8 * kScatterThreads)
+        *reinterpret_cast<uint4*>(row + k) = make_uint4(0, 0, 0, 0);
     const int chunks = K / 8;
     for (int64_t t = blockIdx.x; t < n_tok; t += gridDim.x) {
         __syncthreads();   // the row buffer has been written out (first: idx is there)
