@@ -15,10 +15,11 @@
 //   warp 1      tensor memory and the MMAs (kind::f16, M 128, N 256, K 16)
 //   warps 3..   dequantize the stage's 256 x 64 weights into a bf16 tile in
 //               shared memory, one thread per 64 codes of one weight row; teams
-//               of eight warps take the stages in turn, so that one's hand-over
-//               (waits, fence, arrivals) hides behind another's arithmetic
-//               (three teams 0.66 us per stage of 128 tokens, two 0.77).  After
-//               the sweep they drain the accumulators through the epilogue
+//               of eight warps take the stages in turn and keep a stage's weights
+//               in registers until their buffer is free, so that hand-overs
+//               (waits, fence, arrivals) and MMAs hide behind arithmetic (0.64 us
+//               per stage of 128 tokens; 0.77 with the buffer waited for first).
+//               After the sweep they drain the accumulators through the epilogue
 // linear    the tile's columns are 256 weight rows n, the stage 64 of their k:
 //           the weight tile is K-major.
 // gated     the columns are 128 rows of the gate and the same 128 of the up
@@ -53,9 +54,9 @@ constexpr int BK = 64;                        // contraction per stage
 constexpr int kAStages = 4;
 constexpr int kABytes = TM * BK * 2;          // 16 KB: a stage's tokens
 constexpr int kBBytes = TN * BK * 2;          // 32 KB: one dequantized tile
-constexpr int kTeams = 3;                     // of 8 dequantizing warps, each every third stage
+constexpr int kTeams = 2;                     // of 8 dequantizing warps, on alternate stages
 constexpr int kTeamWarps = 8;
-constexpr int kBBufs = 3;
+constexpr int kBBufs = 4;
 constexpr int kMaxPStages = 6;
 constexpr int kDeqWarps = kTeams * kTeamWarps;
 constexpr int kThreads = 32 * (3 + kDeqWarps);
@@ -549,20 +550,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             uint32_t w[2 * BITS];
             load_words<BITS>(src, w);
+            // the stage's weights wait in registers for their buffer, so that the
+            // arithmetic overlaps the MMAs that still read it
+            uint32_t o[8][4];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                if constexpr (GPT > 1) {
+                    if (c % (8 / GPT) == 0) grp.set(s[c / (8 / GPT)], static_cast<float>(z[c / (8 / GPT)]));
+                }
+                weights8<BITS>(w, c, grp, o[c]);
+            }
             if (!mbar_wait_short(&bars->bempty[b], ((i / kBBufs) & 1u) ^ 1u, abort)) {
                 ok = false;
                 break;
             }
             const uint32_t tile_at = smem_u32(bbuf + b * kBBytes);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                if constexpr (GPT > 1) {
-                    if (c % (8 / GPT) == 0) grp.set(s[c / (8 / GPT)], static_cast<float>(z[c / (8 / GPT)]));
-                }
-                uint32_t o[4];
-                weights8<BITS>(w, c, grp, o);
-                sts128_u(tile_at + dst_off[c], make_uint4(o[0], o[1], o[2], o[3]));
-            }
+            for (int c = 0; c < 8; ++c) sts128_u(tile_at + dst_off[c], make_uint4(o[c][0], o[c][1], o[c][2], o[c][3]));
             fence_async_smem();
             // one arrival per warp (arrivals on a barrier are serialized)
             __syncwarp();
@@ -875,20 +879,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             }
             uint32_t w[BITS];
             load_words<BITS>(src, w);
+            uint32_t o[4][4];   // wait in registers for their buffer, as above
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                if constexpr (TG > 1) {
+                    if (c % (4 / TG) == 0) grp.set(s[c / (4 / TG)], static_cast<float>(z[c / (4 / TG)]));
+                }
+                weights8<BITS>(w, c, grp, o[c]);
+            }
             if (!mbar_wait_short(&bars->bempty[b], ((i / G::kBBufs) & 1u) ^ 1u, abort)) {
                 ok = false;
                 break;
             }
             const uint32_t tile_at = smem_u32(bbuf + b * kPairBBytes);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                if constexpr (TG > 1) {
-                    if (c % (4 / TG) == 0) grp.set(s[c / (4 / TG)], static_cast<float>(z[c / (4 / TG)]));
-                }
-                uint32_t o[4];
-                weights8<BITS>(w, c, grp, o);
-                sts128_u(tile_at + dst_off[c], make_uint4(o[0], o[1], o[2], o[3]));
-            }
+            for (int c = 0; c < 4; ++c) sts128_u(tile_at + dst_off[c], make_uint4(o[c][0], o[c][1], o[c][2], o[c][3]));
             fence_async_smem();
             __syncwarp();
             if (lane == 0) {
