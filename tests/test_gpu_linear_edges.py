@@ -194,6 +194,50 @@ def test_one_layer_as_gate_and_up_and_an_inner_view():
         lt.check(Y, want, bound, form)
 
 
+@pytest.mark.parametrize("form", ["decode", "many"])
+def test_offsets_past_32_bits(form):
+    """Rows of X, residual and Y more than 2^31 elements apart in all."""
+    q = _q()
+    rng = lt.rng_of(13)
+    n, d_col, d_row, pitch = 40, 128, 72, 60_000_000
+    layer = lt.Layer(d_row, d_col, 4, 64, rng)
+    X, res = lt.bf16(rng, n, d_col), lt.bf16(rng, n, d_row)
+    buf = torch.empty(n * pitch, dtype=torch.bfloat16, device="cuda").view(n, pitch)
+    Xv, Rv, Y = buf[:, :d_col], buf[:, 1000:1000 + d_row], buf[:, 2000:2000 + d_row]
+    Xv.copy_(X)
+    Rv.copy_(res)
+    want, bound, _, _ = lt.linear(X, layer, None, form, residual=res)
+    _linear(q, form)(Xv, *layer.cuda(), None, 4, 64, Y, lt.workspace(_sizes(q, form, n, d_col, d_row)), residual=Rv)
+    lt.check(Y, want, bound, "Y")
+
+
+@pytest.mark.parametrize("bits,d_col", [(2, 64), (3, 128), (4, 64), (8, 64)])
+def test_narrowest_layers(bits, d_col):
+    """Packed rows of 16 to 64 bytes: every copy is wider than the layer."""
+    q = _q()
+    rng = lt.rng_of(bits, d_col, 14)
+    layers = [lt.Layer(17, d_col, bits, 8, rng) for _ in range(2)]
+    dev = [t for l in layers for t in l.cuda()]
+    for n in (1, 20, 140, 300):
+        X = lt.bf16(rng, n, d_col)
+        Y = torch.empty(n, 17, dtype=torch.bfloat16, device="cuda")
+        if n <= 20:
+            want, bound, _, _ = lt.gated(X, *layers, None, "decode", "silu")
+            q.gptq_dequant_matmul_gated(X.cuda(), *dev, None, bits, 8, "silu", Y)
+            lt.check(Y, want, bound, f"decode {n}")
+        want, bound, _, _ = lt.gated(X, *layers, None, "many", "silu")
+        q.gptq_dequant_gemm_gated(X.cuda(), *dev, None, bits, 8, "silu", Y,
+                                  lt.workspace(q.gptq_dequant_gemm_gated_workspace_size(n, d_col, 17)))
+        lt.check(Y, want, bound, f"many {n}")
+        dY, g, u = (lt.bf16(rng, n, 17) for _ in range(3))
+        (_, dG), (_, dU) = lt.blank(n, 17, 24), lt.blank(n, 17, 24)
+        dX = torch.empty(n, d_col, dtype=torch.bfloat16, device="cuda")
+        q.gptq_dequant_gemm_gated_backward(dY.cuda(), g.cuda(), u.cuda(), *dev, None, bits, 8, "silu", dG, dU, dX,
+                                           lt.workspace(q.gptq_dequant_gemm_gated_backward_workspace_size(n, d_col, 17)))
+        x, xb = lt.back_product([dG, dU], layers, None)
+        lt.check(dX, x, xb, f"dX {n}")
+
+
 def test_python_refusals():
     q = _q()
     rng = lt.rng_of(12)
