@@ -115,60 +115,101 @@ struct Args {
 };
 
 // ------------------------------------------------------------- epilogue
-// Sixteen consecutive bf16 values (32 bytes, the sector that L2 moves): in one
-// access where the address allows it, else in smaller ones.
-__device__ __forceinline__ void store16(uint16_t* p, const float (&v)[16], int count) {
+// Sixteen consecutive bf16 values per lane (32 bytes, the sector that L2 moves),
+// `count` of them valid (0: none).  Called by whole warps.  Rows on 32- or
+// 16-byte boundaries move in one or two accesses per lane; for any other
+// alignment the warp goes through its 1 KB of shared memory, so that 16 lanes
+// write (read) the 16 values of a row together: alone, a lane's 2-byte stores
+// are as many sector writes (a gated 72 x 775 tile with its products saved took
+// 35 us).
+__device__ __forceinline__ int vector_bytes(const void* p, int count) {
+    // 32, 16 or 0 for the warp
     const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    if (__all_sync(0xffffffffu, count == 0 || (count == 16 && (at & 31) == 0))) return 32;
+    return __all_sync(0xffffffffu, count == 0 || (count == 16 && (at & 15) == 0)) ? 16 : 0;
+}
+__device__ __forceinline__ void store16(uint16_t* p, const float (&v)[16], int count, uint8_t* scratch) {
     uint32_t w[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) w[j] = f32x2_to_bf16x2(v[2 * j], v[2 * j + 1]);
-    if (count == 16 && (at & 31) == 0) {
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
-                     "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                     : "memory");
-    } else if (count == 16 && (at & 15) == 0) {
-        reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (j < count) p[j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
+    const int bytes = vector_bytes(p, count);
+    if (bytes == 32) {
+        if (count > 0)
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
+                         "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                         : "memory");
+        return;
     }
-}
-__device__ __forceinline__ void load16(const uint16_t* p, uint32_t (&w)[8], int count) {
-    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
-    if (count == 16 && (at & 31) == 0) {
-        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-                     : "l"(p)
-                     : "memory");
-    } else if (count == 16 && (at & 15) == 0) {
-        const uint4 x = reinterpret_cast<const uint4*>(p)[0], y = reinterpret_cast<const uint4*>(p)[1];
-        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
-        w[4] = y.x; w[5] = y.y; w[6] = y.z; w[7] = y.w;
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t lo = 2 * j < count ? p[2 * j] : 0u, hi = 2 * j + 1 < count ? p[2 * j + 1] : 0u;
-            w[j] = lo | hi << 16;
+    if (bytes == 16) {
+        if (count > 0) {
+            reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
         }
+        return;
     }
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
+    reinterpret_cast<uint4*>(scratch)[2 * lane] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(scratch)[2 * lane + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+    __syncwarp();
+#pragma unroll 4
+    for (int i = 0; i < 16; ++i) {
+        const int owner = 2 * i + (lane >> 4), idx = lane & 15;
+        uint16_t* q = reinterpret_cast<uint16_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(p), owner));
+        if (idx < __shfl_sync(0xffffffffu, count, owner)) q[idx] = reinterpret_cast<const uint16_t*>(scratch)[owner * 16 + idx];
+    }
+    __syncwarp();
+}
+__device__ __forceinline__ void load16(const uint16_t* p, uint32_t (&w)[8], int count, uint8_t* scratch) {
+    const int bytes = vector_bytes(p, count);
+    if (bytes == 32) {
+        if (count > 0)
+            asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                         : "l"(p)
+                         : "memory");
+        return;
+    }
+    if (bytes == 16) {
+        if (count > 0) {
+            const uint4 x = reinterpret_cast<const uint4*>(p)[0], y = reinterpret_cast<const uint4*>(p)[1];
+            w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+            w[4] = y.x; w[5] = y.y; w[6] = y.z; w[7] = y.w;
+        }
+        return;
+    }
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
+#pragma unroll 4
+    for (int i = 0; i < 16; ++i) {
+        const int owner = 2 * i + (lane >> 4), idx = lane & 15;
+        const uint16_t* q = reinterpret_cast<const uint16_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(p), owner));
+        const bool in = idx < __shfl_sync(0xffffffffu, count, owner);
+        reinterpret_cast<uint16_t*>(scratch)[owner * 16 + idx] = in ? q[idx] : static_cast<uint16_t>(0);
+    }
+    __syncwarp();
+    const uint4 x = reinterpret_cast<const uint4*>(scratch)[2 * lane], y = reinterpret_cast<const uint4*>(scratch)[2 * lane + 1];
+    w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+    w[4] = y.x; w[5] = y.y; w[6] = y.z; w[7] = y.w;
+    __syncwarp();
 }
 
 // Sixteen consecutive outputs of token t from column n on (a multiple of 16): v
 // their sums (gated: of the gate, u of the up matrix), r the residual's words.
+// count: of the 16 that exist (0: a token or column past the end).
+__device__ __forceinline__ int valid16(const Args& a, int t, int n) {
+    return t < a.n_tok && n < a.N ? min(16, a.N - n) : 0;
+}
 template <int MODE>
-__device__ __forceinline__ void load_residual(const Args& a, int t, int n, uint32_t (&r)[8]) {
+__device__ __forceinline__ void load_residual(const Args& a, int t, int n, uint32_t (&r)[8], uint8_t* scratch) {
     if constexpr (MODE == kLinear) {
-        if (a.residual != nullptr && t < a.n_tok && n < a.N)
-            load16(a.residual + t * a.ldr + n, r, min(16, a.N - n));
+        if (a.residual != nullptr) load16(a.residual + t * a.ldr + n, r, valid16(a, t, n), scratch);
     }
 }
 template <int MODE>
 __device__ __forceinline__ void emit16(const Args& a, int t, int n, float (&v)[16], const float (&u)[16],
-                                       const uint32_t (&r)[8]) {
-    const int count = min(16, a.N - n);
-    if (count <= 0) return;
+                                       const uint32_t (&r)[8], uint8_t* scratch) {
+    const int count = valid16(a, t, n);
     if constexpr (MODE == kLinear) {
         if (a.bias != nullptr) {
             if (count == 16 && (reinterpret_cast<uintptr_t>(a.bias) & 15) == 0) {
@@ -183,7 +224,7 @@ __device__ __forceinline__ void emit16(const Args& a, int t, int n, float (&v)[1
                     if (j < count) v[j] += __ldg(a.bias + n + j);
             }
         }
-        if (a.pre[0] != nullptr) store16(a.pre[0] + t * a.ldpre[0] + n, v, count);
+        if (a.pre[0] != nullptr) store16(a.pre[0] + t * a.ldpre[0] + n, v, count, scratch);
         activate_all(v, a.act);
         if (a.residual != nullptr) {
 #pragma unroll
@@ -193,13 +234,13 @@ __device__ __forceinline__ void emit16(const Args& a, int t, int n, float (&v)[1
             }
         }
     } else if constexpr (MODE == kGated) {
-        if (a.pre[0] != nullptr) store16(a.pre[0] + t * a.ldpre[0] + n, v, count);
-        if (a.pre[1] != nullptr) store16(a.pre[1] + t * a.ldpre[1] + n, u, count);
+        if (a.pre[0] != nullptr) store16(a.pre[0] + t * a.ldpre[0] + n, v, count, scratch);
+        if (a.pre[1] != nullptr) store16(a.pre[1] + t * a.ldpre[1] + n, u, count, scratch);
         activate_all(v, a.act);
 #pragma unroll
         for (int j = 0; j < 16; ++j) v[j] *= u[j];
     }
-    store16(a.Y + t * a.ldy + n, v, count);
+    store16(a.Y + t * a.ldy + n, v, count, scratch);
 }
 
 // ------------------------------------------------------- dequantization
@@ -296,9 +337,10 @@ __device__ __forceinline__ void weights8(const uint32_t (&w)[NW], int c, const G
 // WARPS / 4 warps share a lane quarter's chunks of 16 columns.
 template <int MODE, int WARPS>
 __device__ __forceinline__ void drain_tile(const Args& a, uint32_t tmem, int slot, int halves, int t0, int step,
-                                           int n0, int warp, int lane, int row0) {
+                                           int n0, int warp, int lane, int row0, uint8_t* smem) {
     const int q = warp & 3;           // tensor-memory lane quarter of this warp
     const int side = (warp - 3) >> 2;
+    uint8_t* scratch = smem + (warp - 3) * 1024;   // of the rings, which the sweep has left
     const int chunks = MODE == kGated && slot < 0 ? TN / 32 : TN / 16;
 #pragma unroll 1
     for (int e = side; e < halves * chunks; e += WARPS / 4) {
@@ -306,8 +348,8 @@ __device__ __forceinline__ void drain_tile(const Args& a, uint32_t tmem, int slo
         const int t = t0 + h * step + 32 * q + lane;
         const uint32_t at = tmem + (static_cast<uint32_t>(32 * q) << 16) + h * TN + c * 16;
         float v[16], u[16];
-        uint32_t r[8];
-        if (slot < 0) load_residual<MODE>(a, t, n0 + c * 16, r);
+        uint32_t r[8] = {};
+        if (slot < 0) load_residual<MODE>(a, t, n0 + c * 16, r, scratch);
         tmem_ld16(at, v);
         if constexpr (MODE == kGated) {
             if (slot < 0) tmem_ld16(at + TN / 2, u);
@@ -320,10 +362,9 @@ __device__ __forceinline__ void drain_tile(const Args& a, uint32_t tmem, int slo
                              "f"(v[8 * x]), "f"(v[8 * x + 1]), "f"(v[8 * x + 2]), "f"(v[8 * x + 3]), "f"(v[8 * x + 4]),
                              "f"(v[8 * x + 5]), "f"(v[8 * x + 6]), "f"(v[8 * x + 7])
                              : "memory");
-        } else if (t < a.n_tok) {
-            emit16<MODE>(a, t, n0 + c * 16, v, u, r);
         }
         __syncwarp();
+        if (slot < 0) emit16<MODE>(a, t, n0 + c * 16, v, u, r, scratch);
     }
 }
 
@@ -579,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------ drain: tensor memory -> output
         if (ok && mbar_wait_short(&bars->acc_full, 0, abort)) {
             tc_fence_after();
-            drain_tile<MODE, kDeqWarps>(a, tmem, slot, 1, t0, 0, n0, warp, lane, 0);
+            drain_tile<MODE, kDeqWarps>(a, tmem, slot, 1, t0, 0, n0, warp, lane, 0, smem);
         }
     }
 
@@ -904,7 +945,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         // ------------------------------------------------ drain: tensor memory -> output
         if (ok && mbar_wait_short(&bars->acc_full, 0, abort)) {
             tc_fence_after();
-            drain_tile<MODE, kPairDeqWarps>(a, tmem, slot, halves, t0, 256, n0, warp, lane, 128 * rank);
+            drain_tile<MODE, kPairDeqWarps>(a, tmem, slot, halves, t0, 256, n0, warp, lane, 128 * rank, smem);
         }
     }
 
@@ -921,31 +962,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 template <int MODE>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args a, int split_tiles) {
     constexpr int kOut = MODE == kGated ? TN / 2 : TN;
+    __shared__ __align__(16) uint8_t scratch_all[8 * 1024];
+    uint8_t* scratch = scratch_all + (threadIdx.x >> 5) * 1024;
     const int64_t per_tile = static_cast<int64_t>(a.part_rows) * (kOut / 16);
     const int64_t total = per_tile * split_tiles;
-    for (int64_t e = blockIdx.x * 256ll + threadIdx.x; e < total; e += gridDim.x * 256ll) {
+    // whole warps go round together
+    for (int64_t first = blockIdx.x * 256ll + (threadIdx.x & ~31); first < total; first += gridDim.x * 256ll) {
+        const int64_t e = first + (threadIdx.x & 31);
         const int i = static_cast<int>(e / per_tile), x = static_cast<int>(e % per_tile);
         const int row = x / (kOut / 16), c = (x % (kOut / 16)) * 16;
         const int tile = a.full + i;
-        const int t = (tile / a.tiles_n) * a.tile_tokens + row, n = (tile % a.tiles_n) * kOut + c;
-        if (t >= a.n_tok || n >= a.N) continue;
-        uint32_t r[8];
-        load_residual<MODE>(a, t, n, r);
+        const int n = (tile % a.tiles_n) * kOut + c;
+        const int t = e < total ? (tile / a.tiles_n) * a.tile_tokens + row : a.n_tok;   // (past the end: nothing)
+        uint32_t r[8] = {};
+        load_residual<MODE>(a, t, n, r, scratch);
         float v[16] = {}, u[16] = {};
-        const float* p = a.part + (static_cast<int64_t>(i) * a.split * a.part_rows + row) * TN + c;
+        if (valid16(a, t, n) > 0) {
+            const float* p = a.part + (static_cast<int64_t>(i) * a.split * a.part_rows + row) * TN + c;
 #pragma unroll 2
-        for (int k = 0; k < a.split; ++k, p += static_cast<int64_t>(a.part_rows) * TN) {
+            for (int k = 0; k < a.split; ++k, p += static_cast<int64_t>(a.part_rows) * TN) {
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                const float4 q = __ldcs(reinterpret_cast<const float4*>(p) + y);
-                v[4 * y] += q.x; v[4 * y + 1] += q.y; v[4 * y + 2] += q.z; v[4 * y + 3] += q.w;
-                if constexpr (MODE == kGated) {
-                    const float4 w = __ldcs(reinterpret_cast<const float4*>(p + TN / 2) + y);
-                    u[4 * y] += w.x; u[4 * y + 1] += w.y; u[4 * y + 2] += w.z; u[4 * y + 3] += w.w;
+                for (int y = 0; y < 4; ++y) {
+                    const float4 q = __ldcs(reinterpret_cast<const float4*>(p) + y);
+                    v[4 * y] += q.x; v[4 * y + 1] += q.y; v[4 * y + 2] += q.z; v[4 * y + 3] += q.w;
+                    if constexpr (MODE == kGated) {
+                        const float4 w = __ldcs(reinterpret_cast<const float4*>(p + TN / 2) + y);
+                        u[4 * y] += w.x; u[4 * y + 1] += w.y; u[4 * y + 2] += w.z; u[4 * y + 3] += w.w;
+                    }
                 }
             }
         }
-        emit16<MODE>(a, t, n, v, u, r);
+        __syncwarp();
+        emit16<MODE>(a, t, n, v, u, r, scratch);
     }
 }
 
