@@ -51,7 +51,10 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kBlock = 128;          // codes per row and step of a warp
 constexpr int kMaxTok = 32;          // tokens per launch
 constexpr int kMaxDepth = 8;         // blocks of a warp's ring
-constexpr int kSmemTwo = 112 * 1024, kSmemOne = 224 * 1024;   // for two and one CTA per SM
+// Shared memory of two and of one CTA per SM: all of the 228 KB less 1 KB for
+// each CTA.  (With 112 KB the rings of groups of 64 at five to eight tokens missed two
+// blocks by 1 KB and ran with one CTA: 8192 x 8192 34.9 us, now 16.7.)
+constexpr int kSmemTwo = 113 * 1024, kSmemOne = 227 * 1024;
 
 // How groups lie in a block of 128 codes: a block lies in one group; a group
 // is 32 or 64 codes; a group is 8 or 16 codes.
@@ -444,11 +447,12 @@ __global__ void __launch_bounds__(kThreads, NT * MT >= 8 ? 1 : 2)
             }
         } else {
             float c[MT][NT][4], cs[NT][4];
+            const bool g32 = a.g == 32;   // (kNarrow) a group ends with each step, else with every second
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 uint32_t xb[NT][4];
                 tokens(j, xb);
-                if (MODE == kNarrow || j == 0) {
+                if (j == 0 || (MODE == kNarrow && (j == 2 || g32))) {
                     clear(cs);
 #pragma unroll
                     for (int m = 0; m < MT; ++m) clear(c[m]);
@@ -459,7 +463,12 @@ __global__ void __launch_bounds__(kThreads, NT * MT >= 8 ? 1 : 2)
                     Unit<BITS> u[2];
                     units(m, j, u);
                     product(u, xb, 0xffffffffu, c[m]);
-                    if (MODE == kNarrow ? 32 * j < left : j == 3) fold(m, MODE == kNarrow ? 32 * j / a.g : 0, c[m], cs);
+                    if constexpr (MODE == kNarrow) {
+                        // (groups past the last column have no scale: K is a multiple of 64)
+                        if ((g32 || (j & 1)) && 32 * j < left) fold(m, g32 ? j : j >> 1, c[m], cs);
+                    } else {
+                        if (j == 3) fold(m, 0, c[m], cs);
+                    }
                 }
             }
         }
@@ -575,6 +584,12 @@ struct Launch {
     cudaStream_t stream;
 };
 
+// A block in the rings of a CTA's warps: weights and tokens, scales and zero points.
+template <class S>
+int ring_block_bytes(int n_tok, int groups) {
+    return kWarps * ((S::kWBytes + n_tok * 256 + 1023) / 1024 * 1024 + S::kRows * 8 * groups);
+}
+
 template <int BITS, int MODE, int NT, int MT, bool GATED>
 cudaError_t launch_one(Args a, const Launch& l) {
     using S = Shape<BITS, NT, MT>;
@@ -597,7 +612,7 @@ cudaError_t launch_one(Args a, const Launch& l) {
     a.group_magic = bpg > 1 && nblk * (magic * bpg - (uint64_t{1} << 32)) < (uint64_t{1} << 32)
                         ? static_cast<uint32_t>(magic) : 0;
     a.slot_bytes = (S::kWBytes + a.n_tok * 256 + 1023) / 1024 * 1024;
-    const int per = kWarps * (a.slot_bytes + S::kRows * 8 * ngb);
+    const int per = ring_block_bytes<S>(a.n_tok, ngb);
     const int sums = kWarps * a.n_tok * S::kPitch * 4;       // the warps' partial sums
     const int per_sm = NT * MT >= 8 ? 1 : 2, room = (per_sm == 1 ? kSmemOne : kSmemTwo) - S::kHead;
     // More tiles than CTAs run at a time: these go through the tiles in turn, their
@@ -653,9 +668,12 @@ cudaError_t launch_tokens(const Args& a, const Launch& l) {
     // Eight tokens: 64 weight rows per CTA from 4096 rows on (the tokens' work and
     // a block's fixed work are shared by twice the weights: 8192 x 4096 at one
     // token 8.4 against 11.9 us with 32 rows), fewer where 32 rows are needed to
-    // fill the GPU.
-    constexpr int kMany = MODE == kTiny ? 2 : 4;
-    if (a.n_tok <= 8 && (GATED ? 2 : 1) * static_cast<int64_t>(a.N) >= 4096)
+    // fill the GPU or where 64 leave no two blocks in the rings of two CTAs per SM
+    // (8192 x 8192, eight tokens: 8 bits in groups of 64 18.2 against 27.4, 4 bits in groups of 32
+    // 19.6 against 27.7 us).
+    constexpr int kMany = MODE == kTiny || BITS == 8 ? 2 : 4;
+    if (a.n_tok <= 8 && (GATED ? 2 : 1) * static_cast<int64_t>(a.N) >= 4096 &&
+        2 * ring_block_bytes<Shape<BITS, 1, kMany>>(a.n_tok, MODE == kWide ? 1 : kBlock / a.g) <= kSmemTwo - 1024)
         return launch_one<BITS, MODE, 1, kMany, GATED>(a, l);
     if (a.n_tok <= 8) return launch_one<BITS, MODE, 1, 2, GATED>(a, l);
     if (a.n_tok <= 16) return launch_one<BITS, MODE, 2, 2, GATED>(a, l);
