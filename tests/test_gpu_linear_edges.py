@@ -238,6 +238,60 @@ def test_narrowest_layers(bits, d_col):
         lt.check(dX, x, xb, f"dX {n}")
 
 
+# Layers of at least 4096 weight rows take 64 rows per CTA unless two blocks of
+# the rings then leave one CTA per SM; above 148 x 2 x 64 rows a CTA goes through
+# several tiles.  K tails of 64 end inside a block of 128 codes.
+@pytest.mark.parametrize("n,d_col,d_row,bits,g", [
+    (1, 320, 4101, 4, 64), (5, 320, 4101, 4, 64), (8, 4160, 4096, 4, 64), (1, 320, 4101, 4, 32), (4, 2112, 4097, 4, 32),
+    (5, 2112, 4097, 4, 32), (8, 320, 19001, 4, 32), (8, 320, 19001, 4, 64), (2, 256, 38001, 4, -1), (8, 384, 4101, 3, 32),
+    (3, 384, 19001, 3, 64), (8, 320, 4101, 2, 32), (6, 320, 19001, 2, 64), (8, 320, 4101, 8, 128), (1, 320, 19001, 8, 64),
+    (7, 320, 4101, 8, 32), (4, 192, 4101, 4, 16), (8, 192, 4101, 2, 8), (16, 320, 9601, 4, 64), (31, 320, 9601, 4, 32)])
+def test_many_rows_few_tokens(n, d_col, d_row, bits, g):
+    q = _q()
+    rng = lt.rng_of(n, d_col, d_row, bits, g + 2, 15)
+    layers = [lt.Layer(d_row, d_col, bits, g, rng) for _ in range(2)]
+    X, res = lt.bf16(rng, n, d_col), lt.bf16(rng, n, d_row)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    want, bound, _, _ = lt.linear(X, layers[0], None, "decode", None, "gelu", res)
+    buf, Y = lt.blank(n, d_row)
+    q.gptq_dequant_matmul_linear(X.cuda(), *layers[0].cuda(), None, bits, g, Y, activation="gelu", residual=res.cuda(),
+                                 dev_status=st)
+    lt.check(Y, want, bound, "Y")
+    lt.untouched(buf, d_row)
+    want, bound, _, _ = lt.gated(X, *layers, None, "decode", "silu")
+    buf, Y = lt.blank(n, d_row)
+    q.gptq_dequant_matmul_gated(X.cuda(), *layers[0].cuda(), *layers[1].cuda(), None, bits, g, "silu", Y, dev_status=st)
+    lt.check(Y, want, bound, "gated Y")
+    lt.untouched(buf, d_row)
+    assert q.gptq_sync_status(st) == 0
+
+
+@pytest.mark.parametrize("n,d_col,d_row,bits", [(27, 512, 109, 4), (128, 576, 261, 8), (200, 640, 33, 3), (300, 512, 70, 2),
+                                                (700, 1024, 515, 8), (5, 4096, 19, 4)])
+@pytest.mark.parametrize("offset", [0, 1, 8])
+def test_rows_off_their_boundaries(n, d_col, d_row, bits, offset):
+    """Outputs and a residual updated in place whose rows start on 2, 16 or 32
+    bytes, in whole tiles and in tiles whose contraction is split; what lies
+    beside the rows stays."""
+    q = _q()
+    rng = lt.rng_of(n, d_col, d_row, bits, offset, 16)
+    layer = lt.Layer(d_row, d_col, bits, 64, rng)
+    X, res = lt.bf16(rng, n, d_col), lt.bf16(rng, n, d_row)
+    bias = rng.standard_normal(d_row).astype(np.float32)
+    want, bound, pw, pb = lt.linear(X, layer, None, "many", bias, "silu", res)
+    ld = -(-(d_row + 9) // 16) * 16 + (offset & 1)
+    bufs = [torch.full((n, ld), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    Y, pre = (b[:, offset:offset + d_row] for b in bufs)
+    Y.copy_(res)
+    ws = lt.workspace(q.gptq_dequant_gemm_linear_workspace_size(n, d_col, d_row))
+    q.gptq_dequant_gemm_linear(X.cuda(), *layer.cuda(), None, bits, 64, Y, ws, bias=lt.cuda(bias), activation="silu",
+                               residual=Y, pre=pre)
+    lt.check(Y, want, bound, "Y")
+    lt.check(pre, pw, pb, "pre")
+    for b in bufs:
+        assert bool((b[:, :offset] == 7).all()) and bool((b[:, offset + d_row:] == 7).all())
+
+
 def test_python_refusals():
     q = _q()
     rng = lt.rng_of(12)
