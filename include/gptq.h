@@ -410,7 +410,7 @@ typedef enum gptq_activation {
  * launch reads the packed layer once.  W[n][k] = scales[k/g][n] * (code[n][k] -
  * zeros[k/g][n]) enters unrounded, as in gptq_dequant_matmul.  Activations of
  * magnitude 2^64 and more may count as infinite; those below 2^-57 contribute
- * with an absolute error of up to 2^-80 times the weight's scale and codes.
+ * with an absolute error of up to 2^-80 (1 + |zero point|) times the scale.
  *   dev_status  device int32 (may be NULL) receiving GPTQ_ERR_TIMEOUT if a
  *       bounded wait runs out.
  *   ws  gptq_dequant_matmul_linear_workspace_size(n_tok, d_col) bytes, used when

@@ -9,13 +9,15 @@
 // numbers p 2^-133 (subnormal, then the first binade, evenly spaced), so a
 // code masked out of its word, wherever in the low byte of a half word it
 // lies, is q 2^(j - 133) for its bit position j.  The tokens are multiplied by
-// 2^(64 - j) to match (exact), which keeps the sums, 2^-69 of the result, in
-// fp32's normal range; the result is scaled back at the end.  The sums run on
-// the tensor cores (m16n8k16, 16 weight rows by 8 tokens, exact products,
-// fp32 sums), the plain token sum through one more tile whose codes are all 1,
-// so that it lands in the registers that need it.  Tokens of magnitude 2^64
-// and more may overflow; below 2^-57 the products lose relative precision (2^-80
-// absolute).
+// 2^(64 - j) to match (exact), which keeps a group's two sums, 2^-69 of their
+// value, in fp32's normal range; they are scaled back before s enters, so that
+// the outputs' sums have fp32's whole range (scaled back at the end, results
+// below 2^-57 lost bits to fp32's subnormal range).  The sums run on the tensor
+// cores (m16n8k16, 16 weight rows by 8 tokens, exact products, fp32 sums), the
+// plain token sum through one more tile whose codes are all 1, so that it lands
+// in the registers that need it.  Tokens of magnitude 2^64 and more may
+// overflow; below 2^-57 the products x q and x z lose relative precision (2^-80
+// absolute, times s).
 //
 // Bound: the packed layer is read once for up to 32 tokens, so HBM; below
 // about 10 MB the launch and the length of one warp's chain.  What costs after
@@ -39,6 +41,7 @@
 
 #include "activation.cuh"
 #include "common.cuh"
+#include "dequant.cuh"
 #include "kernels.h"
 
 namespace cg = cooperative_groups;
@@ -396,19 +399,32 @@ __global__ void __launch_bounds__(kThreads, NT * MT >= 8 ? 1 : 2)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) c[q][i] = 0.f;
         };
-        // the finished sums of tile m and the block's group enter the outputs
+        // the finished sums of tile m and the block's group enter the outputs, two
+        // tokens at a time: sum - z total, scaled back (exact), times s.  The widest
+        // tiles scale back in scalar instructions, whose factor takes no register
+        // (2 x 28672 x 8192, 32 tokens 165.2 against 168.3 us; with groups of 32
+        // the packed form is ahead, 8192 x 8192 47.2 against 48.1)
         const float* sc = reinterpret_cast<const float*>(sc_ring + slot * sc_bytes) + g8;
         const int32_t* zc = reinterpret_cast<const int32_t*>(sc) + (kRows << ngb_log2);
         auto fold = [&](int m, int grp, const float (&c)[NT][4], const float (&cs)[NT][4]) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const float sv = sc[grp * kRows + m * 16 + 8 * h];
-                const float z = static_cast<float>(zc[grp * kRows + m * 16 + 8 * h]);
+                const float z = -static_cast<float>(zc[grp * kRows + m * 16 + 8 * h]);
+                const uint64_t s2 = pk2(sv, sv), z2 = pk2(z, z);
 #pragma unroll
-                for (int q = 0; q < NT; ++q)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        acc[m][q][2 * h + i] = fmaf(sv, fmaf(-z, cs[q][i], c[q][2 * h + i]), acc[m][q][2 * h + i]);
+                for (int q = 0; q < NT; ++q) {
+                    float* v = acc[m][q] + 2 * h;
+                    uint64_t sum = fma2(z2, pk2(cs[q][0], cs[q][1]), pk2(c[q][2 * h], c[q][2 * h + 1]));
+                    if constexpr (MODE == kWide && NT * MT >= 16) {
+                        float lo, hi;
+                        unpk2(sum, lo, hi);
+                        sum = pk2(lo * kScaleBack, hi * kScaleBack);
+                    } else {
+                        sum = mul2(sum, pk2(kScaleBack, kScaleBack));
+                    }
+                    unpk2(fma2(s2, sum, pk2(v[0], v[1])), v[0], v[1]);
+                }
             }
         };
         // the tokens' values of step j (unit 4j + t), paired like the codes
@@ -528,10 +544,9 @@ __global__ void __launch_bounds__(kThreads, NT * MT >= 8 ? 1 : 2)
                 if constexpr (GATED) u += p[kOut];
             }
         }
-        v *= kScaleBack;
         float y;
         if constexpr (GATED) {
-            y = activate(v, a.act) * (u * kScaleBack);
+            y = activate(v, a.act) * u;
         } else {
             if (a.bias != nullptr) v += a.bias[n];
             y = activate(v, a.act);
