@@ -101,11 +101,14 @@ int64_t gptq_launch_counter(void);
  * it exists so the timeout path can be exercised without a faulty GPU).
  * Arms the NEXT launch of one kernel kind -- 1: the Hessian GEMM of
  * gptq_hessian_accumulate; 2: the next fp32-accurate tensor-core GEMM of any
- * call (gptq_prepare_hinv's first one is its first panel solve) -- so that
- * its MMA-issuing thread first waits, bounded by limit_ns (1 .. 10^9), on a
- * barrier that nothing completes.  That wait runs out like any other: the
- * kernel lets its issued copies and MMAs land (normal limit), frees its
- * tensor memory, writes GPTQ_ERR_TIMEOUT to the call's dev_status and
+ * call (gptq_prepare_hinv's first one is its first panel solve); 4: the decode
+ * form of the products with an epilogue; 5 and 6: their tensor-core kernel
+ * (forward or backward) up to 256 tokens and beyond -- so that its MMA-issuing
+ * thread (4: its first warp) first waits, bounded by limit_ns (1 .. 10^9), on
+ * a barrier that nothing completes.  That wait runs out like any other: the
+ * kernel lets its issued copies and MMAs land (normal limit; 6: the second CTA
+ * of a pair notices by its own waits, 2 s later), frees its tensor memory,
+ * writes GPTQ_ERR_TIMEOUT to the call's dev_status and
  * returns; the call's outputs are then not valid, later calls are
  * unaffected.  One launch consumes the arming.  Never needed in normal use.
  * Errors: GPTQ_ERR_INVALID_ARG for another kernel number or limit.

@@ -741,8 +741,9 @@ def gptq_dequant_gemm_gated_backward_workspace_size(n_tok: int, d_col: int, d_ro
 
 
 def gptq_debug_arm_wait_probe(kernel: int, limit_ns: int) -> None:
-    """Test hook: the next launch of kernel kind 1 (Hessian) or 2 (the next
-    fp32-accurate tensor-core GEMM) waits once, bounded by limit_ns, on a
+    """Test hook: the next launch of kernel kind 1 (Hessian), 2 (the next
+    fp32-accurate tensor-core GEMM) or 4, 5, 6 (the products with an epilogue:
+    decode form, up to 256 tokens, beyond) waits once, bounded by limit_ns, on a
     barrier nothing completes, and reports GPTQ_ERR_TIMEOUT."""
     _check(_lib.gptq_debug_arm_wait_probe(int(kernel), int(limit_ns)),
            "gptq_debug_arm_wait_probe")

@@ -11,19 +11,24 @@ namespace gptq {
 
 namespace {
 std::atomic<int64_t> g_launches{0};
-std::atomic<uint64_t> g_probe[3] = {};
+std::atomic<uint64_t> g_probe[7] = {};
 }
 
 void count_launches(int64_t k) { g_launches.fetch_add(k, std::memory_order_relaxed); }
 
+bool is_probe_kind(int kind) {
+    return kind == kProbeHessian || kind == kProbeGemm || kind == kProbeDecode || kind == kProbeSingle ||
+           kind == kProbePair;
+}
+
 uint64_t take_wait_probe(int kind) {
-    if (kind < 1 || kind > 2) return 0;
+    if (!is_probe_kind(kind)) return 0;
     if (g_probe[kind].load(std::memory_order_relaxed) == 0) return 0;
     return g_probe[kind].exchange(0, std::memory_order_acq_rel);
 }
 
 void arm_wait_probe(int kind, uint64_t ns) {
-    if (kind >= 1 && kind <= 2) g_probe[kind].store(ns, std::memory_order_release);
+    if (is_probe_kind(kind)) g_probe[kind].store(ns, std::memory_order_release);
 }
 
 int64_t launches() { return g_launches.load(std::memory_order_relaxed); }
@@ -140,7 +145,7 @@ const char* gptq_status_string(int32_t status) {
 int32_t gptq_version(void) { return 300; }
 
 gptq_status gptq_debug_arm_wait_probe(int32_t kernel, int64_t limit_ns) {
-    if ((kernel != 1 && kernel != 2) || limit_ns <= 0 || limit_ns > 1000000000) return GPTQ_ERR_INVALID_ARG;
+    if (!gptq::is_probe_kind(kernel) || limit_ns <= 0 || limit_ns > 1000000000) return GPTQ_ERR_INVALID_ARG;
     gptq::arm_wait_probe(kernel, static_cast<uint64_t>(limit_ns));
     return GPTQ_OK;
 }

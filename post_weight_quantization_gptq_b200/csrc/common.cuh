@@ -149,9 +149,17 @@ __device__ __forceinline__ bool mbar_wait_short(uint64_t* bar, uint32_t parity, 
     }
 }
 
+// The answers of a warp's lanes as one: true only where every lane's is.  The
+// lanes wait each on their own, and when a wait runs out some may have seen its
+// phase and others the abort word.  Before a warp's collective (a sync, a vote,
+// a tensor-memory load) they either decide together by this, or a lane whose
+// wait ran out stays in the loop without waiting; otherwise the collective
+// waits for lanes that have left.  Called by whole warps.
+__device__ __forceinline__ bool warp_agree(bool ok) { return __all_sync(0xffffffffu, ok); }
+
 // Timeout probe (a test of the expiry path, armed from the host through
 // gptq_debug_arm_wait_probe): when probe_ns > 0 the kernel's MMA-issuing
-// thread first waits, bounded by probe_ns, on a barrier that nothing ever
+// thread (the decode form: its first warp) first waits, bounded by probe_ns, on a barrier that nothing ever
 // arrives on.  The wait runs out, raises *abort and the kernel winds down
 // exactly as after any expired wait (issued copies and MMAs still land under
 // the normal limit) and reports GPTQ_ERR_TIMEOUT.  Returns false then.

@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(&bars->pempty[ps]);
         }
         // ------------------------------------------------ drain: TMEM -> Y
-        if (ok && mbar_wait(&bars->acc_full, 0, abort)) {
+        if (warp_agree(ok && mbar_wait(&bars->acc_full, 0, abort))) {
             tc_fence_after();
             const int q = warp & 3;           // TMEM lane quarter of this warp
             const int h = (warp - 2) >> 2;    // accumulator (token half)

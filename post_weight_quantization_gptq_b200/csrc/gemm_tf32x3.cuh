@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 static_assert(Sched::kRmw == (Epi == kEpiReduce),
                               "reduce serves read-modify-write outputs, store plain ones");
                 constexpr float sgn = Epi == kEpiReduce ? -1.f : 1.f;
-                if (!mbar_wait(&bars->acc_full[slot], use & 1u, abort)) break;
+                if (!warp_agree(mbar_wait(&bars->acc_full[slot], use & 1u, abort))) break;
                 tc_fence_after();
                 const uint32_t rbase = smem_u32(smem + kStages * kStageBytes + 1024) + q * 2 * kRedBufBytes;
 #pragma unroll
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     fetch(1, old[1]);
                 }
             }
-            if (!mbar_wait(&bars->acc_full[slot], use & 1u, abort)) break;
+            if (!warp_agree(mbar_wait(&bars->acc_full[slot], use & 1u, abort))) break;
             tc_fence_after();
 #pragma unroll
             for (int cc = 0; cc < BN / 32; ++cc) {

@@ -260,10 +260,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------ epilogue warps 2..9
         const int q = warp & 3;  // TMEM lane quarter this warp may access
         const int half = (warp - 2) >> 2;  // which 128 of each accumulator's 256 columns it drains
-        for (int w = 0; w < waves && !*abort; ++w) {
+        for (int w = 0; w < waves; ++w) {
             const int t = blockIdx.x + (w / nchunk) * G;
             if (t >= num_blocks) break;
-            if (!mbar_wait(&bars->acc_full, w & 1, abort)) break;
+            if (!warp_agree(!*abort && mbar_wait(&bars->acc_full, w & 1, abort))) break;
             tc_fence_after();
             int pi, nj;
             block_coords(t, NT, pi, nj);

@@ -20,7 +20,8 @@ int64_t launches();
 
 // Timeout probes armed by gptq_debug_arm_wait_probe: the limit (ns) for the
 // next launch of the kernel kind, 0 when unarmed; taking it disarms it.
-enum ProbeKind { kProbeHessian = 1, kProbeGemm = 2 };
+enum ProbeKind { kProbeHessian = 1, kProbeGemm = 2, kProbeDecode = 4, kProbeSingle = 5, kProbePair = 6 };
+bool is_probe_kind(int kind);
 uint64_t take_wait_probe(int kind);
 
 // Launch with the programmatic-serialization attribute when pdl is set; an

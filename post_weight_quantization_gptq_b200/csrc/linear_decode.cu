@@ -80,6 +80,7 @@ struct Args {
     int blocks_per_group;    // (kWide)
     uint32_t group_magic;    // block / blocks_per_group = high word of block * group_magic; 0: divide
     int32_t* status;
+    uint64_t probe_ns;
 };
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -214,7 +215,9 @@ __global__ void __launch_bounds__(kThreads, NT * MT >= 8 ? 1 : 2)
     constexpr int kOut = 16 * kTilesM;                       // outputs of the CTA
     extern __shared__ __align__(1024) uint8_t sm[];
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm);        // [kWarps][kMaxDepth]
-    int* abort_word = reinterpret_cast<int*>(bars + kWarps * kMaxDepth);
+    uint64_t* never = bars + kWarps * kMaxDepth;             // (timeout probe)
+    int* abort_word = reinterpret_cast<int*>(never + 1);
+    int* stopped = abort_word + 1;                           // [kWarps]: lane 0's first block that did not come
     volatile int* abort = abort_word;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -291,7 +294,11 @@ __global__ void __launch_bounds__(kThreads, NT * MT >= 8 ? 1 : 2)
 
     if (lane == 0) {
         for (int d = 0; d < depth; ++d) mbar_init(&full[d], 1);
-        if (warp == 0) *abort_word = 0;
+        stopped[warp] = 0;
+        if (warp == 0) {
+            mbar_init(never, 1);
+            *abort_word = 0;
+        }
         fence_barrier_init();
         fence_async_smem();
         if (warp == 0) {
@@ -348,6 +355,7 @@ __global__ void __launch_bounds__(kThreads, NT * MT >= 8 ? 1 : 2)
     uint32_t phase = 0;
     bool ok = true;
     int done = 0;   // blocks consumed
+    if (a.probe_ns != 0 && warp == 0) ok = wait_probe(never, a.probe_ns, abort);
     float* red = reinterpret_cast<float*>(sm + a.red_at);    // [kWarps][n_tok][kPitch]
     cg::cluster_group cluster = cg::this_cluster();
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
@@ -358,10 +366,11 @@ __global__ void __launch_bounds__(kThreads, NT * MT >= 8 ? 1 : 2)
         for (int q = 0; q < NT; ++q)
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[m][q][i] = 0.f;
-    for (int s = 0; s < steps && ok; ++s, ++done) {
-        if (!mbar_wait_short(&full[slot], phase, abort)) {
+    for (int s = 0; s < steps; ++s, ++done) {
+        // a lane whose wait runs out stays with its warp, whatever it then reads
+        if (ok && !mbar_wait_short(&full[slot], phase, abort)) {
             ok = false;
-            break;
+            if (lane == 0) stopped[warp] = done;
         }
         cp_wait(depth - 1);
         __syncwarp();
@@ -490,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, NT * MT >= 8 ? 1 : 2)
         }
         __syncwarp();   // every lane has read the slot
         if (done + depth < items) {
-            if (lane == 0) {
+            if (lane == 0 && ok) {
                 load_weights(next_s, next_n0, slot);
                 load_tokens(next_s, slot);
             }
@@ -559,10 +568,11 @@ __global__ void __launch_bounds__(kThreads, NT * MT >= 8 ? 1 : 2)
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (!ok && lane == 0) {
-        // never leave with copies in flight (bounded): blocks `done` on, as far
-        // as they were issued
+        // never leave with copies in flight (bounded): from that block on, as far as
+        // they were issued
         volatile int no_abort = 0;
-        for (int i = done; i < items && i < done + depth; ++i)
+        const int from = stopped[warp];
+        for (int i = from; i < items && i < from + depth; ++i)
             if (!mbar_wait(&full[i % depth], (i / depth) & 1u, &no_abort)) break;
     }
     if (threadIdx.x == 0 && *abort) report(a.status, GPTQ_ERR_TIMEOUT);
@@ -626,6 +636,7 @@ cudaError_t launch_one(Args a, const Launch& l) {
     const uint64_t magic = bpg > 1 ? ((uint64_t{1} << 32) + bpg - 1) / bpg : 0;
     a.group_magic = bpg > 1 && nblk * (magic * bpg - (uint64_t{1} << 32)) < (uint64_t{1} << 32)
                         ? static_cast<uint32_t>(magic) : 0;
+    a.probe_ns = take_wait_probe(kProbeDecode);
     a.slot_bytes = (S::kWBytes + a.n_tok * 256 + 1023) / 1024 * 1024;
     const int per = ring_block_bytes<S>(a.n_tok, ngb);
     const int sums = kWarps * a.n_tok * S::kPitch * 4;       // the warps' partial sums

@@ -92,9 +92,11 @@ struct Bars {
     uint64_t pfull[kMaxPStages], pempty[kMaxPStages];
     uint64_t bfull[kBBufs], bempty[kBBufs];
     uint64_t acc_full, drain;
+    uint64_t never;                             // (timeout probe)
     uint32_t tmem;
     int abort;
 };
+static_assert(sizeof(Bars) <= 256, "their share of kSmem");
 
 struct Args {
     PackedMatrix mat[2];
@@ -116,6 +118,7 @@ struct Args {
     uint16_t* Y;
     int64_t ldy;
     int32_t* status;
+    uint64_t probe_ns;
 };
 
 // ------------------------------------------------------------- epilogue
@@ -418,6 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(&bars->acc_full, 1);
         mbar_init(&bars->drain, 1);
+        mbar_init(&bars->never, 1);
         bars->abort = 0;
         fence_barrier_init();
         tma_prefetch_desc(&tma0);
@@ -492,8 +496,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------ MMA issuer
         if (lane == 0) {
             constexpr uint32_t kIdesc = instr_desc(/*bf16*/ 1, /*A K-major*/ 0, /*B*/ MODE == kBack ? 1 : 0, 128, TN);
-            bool ok = true;
-            for (int i = 0; i < k1 - k0; ++i) {
+            bool ok = wait_probe(&bars->never, a.probe_ns, abort);
+            for (int i = 0; ok && i < k1 - k0; ++i) {
                 const int st = i % kAStages, b = i % kBBufs;
                 if (!mbar_wait_short(&bars->afull[st], (i / kAStages) & 1u, abort) ||
                     !mbar_wait_short(&bars->bfull[b], (i / kBBufs) & 1u, abort)) {
@@ -573,6 +577,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t dst_off[8];
 #pragma unroll
         for (int c = 0; c < 8; ++c) dst_off[c] = j * 128 + ((c ^ (j & 7)) << 4);
+        // a lane whose wait runs out stays with its warp, writes what it has and
+        // reports nothing more
         bool ok = true;
         for (int it = k0 + team, i = team; it < k1; it += kTeams, i += kTeams) {
             const int pi = G::kPairs ? i >> 1 : i;
@@ -584,10 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             fetch(it + kTeams);
             if constexpr (GPT == 1) grp.set(s[0], static_cast<float>(z[0]));
-            if (!mbar_wait_short(&bars->pfull[ps], (pi / G::kPStages) & 1u, abort)) {
-                ok = false;
-                break;
-            }
+            ok = ok && mbar_wait_short(&bars->pfull[ps], (pi / G::kPStages) & 1u, abort);
             const uint8_t* src = pbuf + ps * G::kSlot;
             if constexpr (BITS != 3) {
                 src += j * G::kRowBytes;
@@ -608,24 +611,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 weights8<BITS>(w, c, grp, o[c]);
             }
-            if (!mbar_wait_short(&bars->bempty[b], ((i / kBBufs) & 1u) ^ 1u, abort)) {
-                ok = false;
-                break;
-            }
+            ok = ok && mbar_wait_short(&bars->bempty[b], ((i / kBBufs) & 1u) ^ 1u, abort);
             const uint32_t tile_at = smem_u32(bbuf + b * kBBytes);
 #pragma unroll
             for (int c = 0; c < 8; ++c) sts128_u(tile_at + dst_off[c], make_uint4(o[c][0], o[c][1], o[c][2], o[c][3]));
             fence_async_smem();
             // one arrival per warp (arrivals on a barrier are serialized)
             __syncwarp();
-            if (lane == 0) {
+            if (lane == 0 && ok) {
                 mbar_arrive(&bars->bfull[b]);
                 // the slot's words have been used (their loads completed) before it may be refilled
                 mbar_arrive(&bars->pempty[ps]);
             }
         }
         // ------------------------------------------------ drain: tensor memory -> output
-        if (ok && mbar_wait_short(&bars->acc_full, 0, abort)) {
+        if (warp_agree(ok && mbar_wait_short(&bars->acc_full, 0, abort))) {
             tc_fence_after();
             drain_tile<MODE, kDeqWarps>(a, tmem, slot, 1, t0, 0, n0, warp, lane, 0, smem);
         }
@@ -679,9 +679,11 @@ struct PairBars {
     uint64_t pfull[8], pempty[8];
     uint64_t ready[kPairBBufs], bempty[kPairBBufs];               // ready: rank 0's, arrivals of both CTAs
     uint64_t acc_full, drain;
+    uint64_t never;                             // (timeout probe)
     uint32_t tmem;
     int abort;
 };
+static_assert(sizeof(PairBars) <= 512, "their share of kSmem");
 
 template <int BITS, int GPT, int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
@@ -727,6 +729,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
         mbar_init(&bars->acc_full, 1);
         mbar_init(&bars->drain, 1);
+        mbar_init(&bars->never, 1);
         bars->abort = 0;
         fence_barrier_init();
         tma_prefetch_desc(&tma0);
@@ -802,8 +805,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         // ------------------------------------------------ MMA issuer (for both CTAs)
         if (lane == 0 && rank == 0) {
             constexpr uint32_t kIdesc = instr_desc(/*bf16*/ 1, /*A K-major*/ 0, /*B*/ MODE == kBack ? 1 : 0, 256, TN);
-            bool ok = true;
-            for (int i = 0; i < k1 - k0; ++i) {
+            bool ok = wait_probe(&bars->never, a.probe_ns, abort);
+            for (int i = 0; ok && i < k1 - k0; ++i) {
                 const int st = i % depth, b = i % G::kBBufs;
                 if (!mbar_wait_short(&bars->afull[st], (i / depth) & 1u, abort) ||
                     !mbar_wait_cluster(&bars->peer[st], (i / depth) & 1u, abort) ||
@@ -902,6 +905,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         uint32_t dst_off[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) dst_off[c] = j * 128 + (((4 * part + c) ^ (j & 7)) << 4);
+        // a lane whose wait runs out stays with its warp, writes what it has and
+        // reports nothing more
         bool ok = true;
         for (int it = k0 + team, i = team; it < k1; it += kPairTeams, i += kPairTeams) {
             const int pi = G::kPairs ? i >> 1 : i;
@@ -913,10 +918,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             }
             fetch(it + kPairTeams);
             if constexpr (TG == 1) grp.set(s[0], static_cast<float>(z[0]));
-            if (!mbar_wait_short(&bars->pfull[ps], (pi / G::kPStages) & 1u, abort)) {
-                ok = false;
-                break;
-            }
+            ok = ok && mbar_wait_short(&bars->pfull[ps], (pi / G::kPStages) & 1u, abort);
             const uint8_t* src = pbuf + ps * G::kSlot + part * (4 * BITS);
             if constexpr (BITS != 3) {
                 src += j * G::kRowBytes;
@@ -935,22 +937,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 }
                 weights8<BITS>(w, c, grp, o[c]);
             }
-            if (!mbar_wait_short(&bars->bempty[b], ((i / G::kBBufs) & 1u) ^ 1u, abort)) {
-                ok = false;
-                break;
-            }
+            ok = ok && mbar_wait_short(&bars->bempty[b], ((i / G::kBBufs) & 1u) ^ 1u, abort);
             const uint32_t tile_at = smem_u32(bbuf + b * kPairBBytes);
 #pragma unroll
             for (int c = 0; c < 4; ++c) sts128_u(tile_at + dst_off[c], make_uint4(o[c][0], o[c][1], o[c][2], o[c][3]));
             fence_async_smem();
             __syncwarp();
-            if (lane == 0) {
+            if (lane == 0 && ok) {
                 mbar_arrive_cluster(&bars->ready[b], 0);
                 mbar_arrive(&bars->pempty[ps]);
             }
         }
         // ------------------------------------------------ drain: tensor memory -> output
-        if (ok && mbar_wait_short(&bars->acc_full, 0, abort)) {
+        if (warp_agree(ok && mbar_wait_short(&bars->acc_full, 0, abort))) {
             tc_fence_after();
             drain_tile<MODE, kPairDeqWarps>(a, tmem, slot, halves, t0, 256, n0, warp, lane, 128 * rank, smem);
         }
@@ -1081,6 +1080,7 @@ gptq_status run(Args a, const CUtensorMap (&ta)[2], const uint32_t* const (&pack
     a.full = p.full; a.split = p.split; a.per = p.per; a.part_rows = p.part_rows;
     a.tile_tokens = p.tile_tokens;
     a.part = static_cast<float*>(part);
+    a.probe_ns = take_wait_probe(p.pair ? kProbePair : kProbeSingle);
     const int rest = p.tiles_n * p.tiles_t - p.full;
     const int units = p.full + rest * p.split;
     // the packed words move as raw 32-bit elements (the map's fp32 type only sizes them)
