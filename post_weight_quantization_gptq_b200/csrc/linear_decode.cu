@@ -409,10 +409,9 @@ __global__ void __launch_bounds__(kThreads, NT * MT >= 8 ? 1 : 2)
                 for (int i = 0; i < 4; ++i) c[q][i] = 0.f;
         };
         // the finished sums of tile m and the block's group enter the outputs, two
-        // tokens at a time: sum - z total, scaled back (exact), times s.  The widest
-        // tiles scale back in scalar instructions, whose factor takes no register
-        // (2 x 28672 x 8192, 32 tokens 165.2 against 168.3 us; with groups of 32
-        // the packed form is ahead, 8192 x 8192 47.2 against 48.1)
+        // tokens at a time: sum - z total, scaled back (exact), times s (in scalar
+        // instructions the scaling cost 8192 x 8192 with groups of 32 6 % at 32
+        // tokens; packed, 3 %)
         const float* sc = reinterpret_cast<const float*>(sc_ring + slot * sc_bytes) + g8;
         const int32_t* zc = reinterpret_cast<const int32_t*>(sc) + (kRows << ngb_log2);
         auto fold = [&](int m, int grp, const float (&c)[NT][4], const float (&cs)[NT][4]) {
@@ -420,19 +419,12 @@ __global__ void __launch_bounds__(kThreads, NT * MT >= 8 ? 1 : 2)
             for (int h = 0; h < 2; ++h) {
                 const float sv = sc[grp * kRows + m * 16 + 8 * h];
                 const float z = -static_cast<float>(zc[grp * kRows + m * 16 + 8 * h]);
-                const uint64_t s2 = pk2(sv, sv), z2 = pk2(z, z);
+                const uint64_t s2 = pk2(sv, sv), z2 = pk2(z, z), back = pk2(kScaleBack, kScaleBack);
 #pragma unroll
                 for (int q = 0; q < NT; ++q) {
                     float* v = acc[m][q] + 2 * h;
-                    uint64_t sum = fma2(z2, pk2(cs[q][0], cs[q][1]), pk2(c[q][2 * h], c[q][2 * h + 1]));
-                    if constexpr (MODE == kWide && NT * MT >= 16) {
-                        float lo, hi;
-                        unpk2(sum, lo, hi);
-                        sum = pk2(lo * kScaleBack, hi * kScaleBack);
-                    } else {
-                        sum = mul2(sum, pk2(kScaleBack, kScaleBack));
-                    }
-                    unpk2(fma2(s2, sum, pk2(v[0], v[1])), v[0], v[1]);
+                    const uint64_t sum = fma2(z2, pk2(cs[q][0], cs[q][1]), pk2(c[q][2 * h], c[q][2 * h + 1]));
+                    unpk2(fma2(s2, mul2(sum, back), pk2(v[0], v[1])), v[0], v[1]);
                 }
             }
         };
