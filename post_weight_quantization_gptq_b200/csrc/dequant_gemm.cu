@@ -426,10 +426,9 @@ cudaError_t launch_gather(const uint16_t* X, int64_t ldx, int64_t n_tok, int K,
     const size_t smem = static_cast<size_t>(K) * 2;
     const bool vec = (ldx % 8) == 0 && (reinterpret_cast<uintptr_t>(X) & 15) == 0;
     const size_t piped = 3 * smem;  // indices and two rows
-    if (vec && piped <= 227 * 1024 && K <= 65536) {
+    if (vec && piped <= kMaxDynamicSmem && K <= 65536) {
         auto kern = gather_bf16_piped_kernel;
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(piped));
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamicSmem);
         if (e != cudaSuccess) return e;
         // as many CTAs as fit: with one per SM a few hundred rows were a chain of
         // three or four rows each (500 x 11008: 10.3 us)
@@ -448,8 +447,7 @@ cudaError_t launch_gather(const uint16_t* X, int64_t ldx, int64_t n_tok, int K,
         return cudaGetLastError();
     }
     auto kern = vec ? gather_bf16_kernel<true, true> : gather_bf16_kernel<true, false>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kGatherSmemMax);
     if (e != cudaSuccess) return e;
     int per_sm = 0;
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kGatherThreads, smem);

@@ -24,6 +24,12 @@ enum ProbeKind { kProbeHessian = 1, kProbeGemm = 2, kProbeDecode = 4, kProbeSing
 bool is_probe_kind(int kind);
 uint64_t take_wait_probe(int kind);
 
+// Dynamic shared memory a CTA may have.  A kernel whose launches need different
+// amounts is raised to a constant bound of them, never to the one of this
+// launch: the attribute belongs to the kernel, and another host thread may set
+// it between this thread's call and its launch.
+constexpr int kMaxDynamicSmem = 227 * 1024;
+
 // Launch with the programmatic-serialization attribute when pdl is set; an
 // ordinary launch otherwise.  Such a kernel calls pdl_wait() before its first
 // global memory access, and reads data an earlier kernel wrote only through

@@ -237,8 +237,7 @@ gptq_status launch_scatter(const uint16_t* dXq, int64_t n_tok, int d_col, const 
     const size_t smem = static_cast<size_t>(d_col) * 4;
     if (d_col <= 65536 && smem <= kScatterSmem) {
         auto kern = scatter_kernel<true>;
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
-            cudaSuccess)
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kScatterSmem) != cudaSuccess)
             return GPTQ_ERR_CUDA;
         int per_sm = 0;
         if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kScatterThreads, smem) != cudaSuccess)

@@ -57,7 +57,7 @@ constexpr int kMaxDepth = 8;         // blocks of a warp's ring
 // Shared memory of two and of one CTA per SM: all of the 228 KB less 1 KB for
 // each CTA.  (With 112 KB the rings of groups of 64 at five to eight tokens missed two
 // blocks by 1 KB and ran with one CTA: 8192 x 8192 34.9 us, now 16.7.)
-constexpr int kSmemTwo = 113 * 1024, kSmemOne = 227 * 1024;
+constexpr int kSmemTwo = 113 * 1024, kSmemOne = kMaxDynamicSmem;
 
 // How groups lie in a block of 128 codes: a block lies in one group; a group
 // is 32 or 64 codes; a group is 8 or 16 codes.
@@ -648,7 +648,7 @@ cudaError_t launch_one(Args a, const Launch& l) {
     if (a.depth > items) a.depth = items;
     a.red_at = turns ? S::kHead + a.depth * per : S::kHead;
     const int smem = turns || a.depth * per < sums ? a.red_at + sums : S::kHead + a.depth * per;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemOne);
     if (e != cudaSuccess) return e;
     constexpr Swz kSwz = BITS == 8 ? Swz::k128 : BITS == 4 ? Swz::k64 : BITS == 2 ? Swz::k32 : Swz::kNone;
     const uint64_t words = static_cast<uint64_t>(a.K) * BITS / 32;

@@ -612,7 +612,7 @@ gptq_status launch_quantize(float* W, int64_t d_row, int64_t d_col, int64_t ldw,
     if (permuted) {
         const size_t row_smem = static_cast<size_t>(d_col) * sizeof(float);
         if (cudaFuncSetAttribute(permute_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(row_smem)) != cudaSuccess)
+                                 kMaxDynamicSmem) != cudaSuccess)
             return GPTQ_ERR_CUDA;
         const int prow_grid = static_cast<int>(d_row < 4 * num_sms() ? d_row : 4 * num_sms());
         permute_rows_kernel<<<prow_grid, 256, row_smem, stream>>>(W, d_row, d_col, ldw, perm, dead,
