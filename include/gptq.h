@@ -452,7 +452,8 @@ size_t gptq_dequant_matmul_gated_workspace_size(int64_t n_tok, int64_t d_col);
  *   ws      *_workspace_size(n_tok, d_col, d_row) bytes: the tokens in
  *           quantization order (perm given, or X's rows not 16-byte aligned) and
  *           the parts of output tiles whose contraction is split over several
- *           SMs.  May be NULL where neither happens.
+ *           SMs.  May be NULL where neither happens.  A workspace for n_tok
+ *           tokens serves every call of that layer with fewer.
  */
 gptq_status gptq_dequant_gemm_linear(const uint16_t *X, int64_t n_tok, int64_t d_col, int64_t ldx,
                                      const uint32_t *packed, const float *scales,
@@ -472,7 +473,7 @@ gptq_status gptq_dequant_gemm_gated(const uint16_t *X, int64_t n_tok, int64_t d_
                                     int64_t ldy, int32_t *dev_status, void *ws, size_t ws_bytes,
                                     cudaStream_t stream);
 
-/* Workspace bytes of the two; 0 for invalid sizes. */
+/* Workspace bytes of the two, which do not fall as n_tok grows; 0 for invalid sizes. */
 size_t gptq_dequant_gemm_linear_workspace_size(int64_t n_tok, int64_t d_col, int64_t d_row);
 size_t gptq_dequant_gemm_gated_workspace_size(int64_t n_tok, int64_t d_col, int64_t d_row);
 
@@ -500,7 +501,8 @@ size_t gptq_dequant_gemm_gated_workspace_size(int64_t n_tok, int64_t d_col, int6
  *           buffers).
  *   dev_status  as above.
  *   ws      *_workspace_size(n_tok, d_col, d_row) bytes, used with a
- *           permutation, with dbias and for split tiles.
+ *           permutation, with dbias and for split tiles; one for n_tok tokens
+ *           serves every call of that layer with fewer.
  *   n_tok == 0 writes nothing but a zero dbias.
  */
 gptq_status gptq_dequant_gemm_linear_backward(
@@ -518,7 +520,7 @@ gptq_status gptq_dequant_gemm_gated_backward(
     uint16_t *dUp, int64_t lddup, uint16_t *dX, int64_t lddx, int32_t *dev_status, void *ws,
     size_t ws_bytes, cudaStream_t stream);
 
-/* Workspace bytes of the two; 0 for invalid sizes. */
+/* Workspace bytes of the two, which do not fall as n_tok grows; 0 for invalid sizes. */
 size_t gptq_dequant_gemm_linear_backward_workspace_size(int64_t n_tok, int64_t d_col,
                                                         int64_t d_row);
 size_t gptq_dequant_gemm_gated_backward_workspace_size(int64_t n_tok, int64_t d_col, int64_t d_row);

@@ -179,6 +179,7 @@ struct BackwardCall {
     void* ws;
 };
 size_t bias_partial_bytes(int64_t n_tok, int64_t d_row);
+size_t most_bias_partial_bytes(int64_t n_tok, int64_t d_row);
 gptq_status launch_slopes(const BackwardCall& c, float* bias_part, int64_t* launches, cudaStream_t stream);
 gptq_status launch_scatter(const uint16_t* dXq, int64_t n_tok, int d_col, const int32_t* perm, uint16_t* dX,
                            int64_t lddx, cudaStream_t stream);

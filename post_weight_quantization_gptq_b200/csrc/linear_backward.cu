@@ -209,6 +209,12 @@ size_t bias_partial_bytes(int64_t n_tok, int64_t d_row) {
     return static_cast<size_t>(slabs(n_tok)) * d_row * sizeof(float);
 }
 
+// The most of any batch of up to n_tok tokens.
+size_t most_bias_partial_bytes(int64_t n_tok, int64_t d_row) {
+    const int64_t s = (n_tok + kSlab - 1) / kSlab;
+    return static_cast<size_t>(s < kMaxSlabs ? s : kMaxSlabs) * d_row * sizeof(float);
+}
+
 gptq_status launch_slopes(const BackwardCall& c, float* bias_part, int64_t* launches, cudaStream_t stream) {
     const bool gated = c.mat[1].packed != nullptr;
     if (!gated && c.dP[0] == nullptr && bias_part == nullptr) return GPTQ_OK;   // dY is the gradient

@@ -1048,6 +1048,24 @@ Plan make_plan(int64_t n_tok, int64_t N, int nk, bool gated, bool pairs) {
     return p;
 }
 
+// Most bytes of partial tiles that any batch of up to n_tok tokens leaves, at
+// either kind of packed slot.  They go up and down with the tokens: a part's rows
+// grow up to a tile, and how many tiles the last wave holds repeats itself after
+// `slots` rows of tiles.
+size_t most_part_bytes(int64_t n_tok, int64_t N, int nk, bool gated) {
+    size_t most = 0;
+    auto take = [&](int64_t n) {
+        for (const bool pairs : {false, true}) {
+            const size_t b = make_plan(n < n_tok ? n : n_tok, N, nk, gated, pairs).part_bytes;
+            if (b > most) most = b;
+        }
+    };
+    for (int64_t n = TM; n - TM < n_tok && n < kPairTokens; n += TM) take(n);
+    for (int64_t n = PM; n - PM < n_tok && n <= static_cast<int64_t>(PM) * (kSms / 2 + 1) && n_tok >= kPairTokens; n += PM)
+        take(n);
+    return most;
+}
+
 template <int BITS, int GPT, int MODE>
 cudaError_t launch_one(const CUtensorMap (&ta)[2], const CUtensorMap (&tp)[2], const Args& a, int units,
                        cudaStream_t stream) {
@@ -1114,10 +1132,8 @@ size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 }  // namespace
 
 size_t linear_gemm_workspace_bytes(int64_t n_tok, int64_t d_col, int64_t d_row, bool gated) {
-    const Plan p = make_plan(n_tok, d_row, static_cast<int>(d_col / BK), gated, true);
-    const Plan q = make_plan(n_tok, d_row, static_cast<int>(d_col / BK), gated, false);
     return round256(static_cast<size_t>(n_tok) * d_col * 2) +
-           round256(p.part_bytes > q.part_bytes ? p.part_bytes : q.part_bytes);
+           round256(most_part_bytes(n_tok, d_row, static_cast<int>(d_col / BK), gated));
 }
 
 gptq_status launch_linear_gemm(const LinearCall& c, cudaStream_t stream) {
@@ -1176,9 +1192,9 @@ int back_stages(int64_t d_row, bool gated) { return static_cast<int>((d_row + BK
 }  // namespace
 
 size_t linear_backward_workspace_bytes(int64_t n_tok, int64_t d_col, int64_t d_row, bool gated) {
-    const Plan p = make_plan(n_tok, d_col, back_stages(d_row, gated), false, false);
-    return round256(static_cast<size_t>(n_tok) * d_col * 2) + round256(p.part_bytes) +
-           (gated ? 0 : round256(bias_partial_bytes(n_tok, d_row)));
+    return round256(static_cast<size_t>(n_tok) * d_col * 2) +
+           round256(most_part_bytes(n_tok, d_col, back_stages(d_row, gated), false)) +
+           (gated ? 0 : round256(most_bias_partial_bytes(n_tok, d_row)));
 }
 
 gptq_status launch_linear_backward(const BackwardCall& c, cudaStream_t stream) {
