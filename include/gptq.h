@@ -449,11 +449,11 @@ size_t gptq_dequant_matmul_gated_workspace_size(int64_t n_tok, int64_t d_col);
  *   gate, up  gated, each or NULL: the two products, the same way.
  *   dev_status  device int32 (may be NULL) receiving GPTQ_ERR_TIMEOUT if a
  *           bounded wait runs out.
- *   ws      *_workspace_size(n_tok, d_col, d_row) bytes: the tokens in
- *           quantization order (perm given, or X's rows not 16-byte aligned) and
- *           the parts of output tiles whose contraction is split over several
- *           SMs.  May be NULL where neither happens.  A workspace for n_tok
- *           tokens serves every call of that layer with fewer.
+ *   ws      the parts of output tiles whose contraction is split over several
+ *           SMs, and the tokens in quantization order (perm given, or X's rows
+ *           not 16-byte aligned; n_tok * d_col * 2 bytes rounded up to 256).
+ *           May be NULL where neither happens.  *_workspace_size(n_tok, d_col,
+ *           d_row) bytes serve every call of that layer with up to n_tok tokens.
  */
 gptq_status gptq_dequant_gemm_linear(const uint16_t *X, int64_t n_tok, int64_t d_col, int64_t ldx,
                                      const uint32_t *packed, const float *scales,
@@ -500,9 +500,9 @@ size_t gptq_dequant_gemm_gated_workspace_size(int64_t n_tok, int64_t d_col, int6
  *           read as k and the values are then unspecified; no access leaves the
  *           buffers).
  *   dev_status  as above.
- *   ws      *_workspace_size(n_tok, d_col, d_row) bytes, used with a
- *           permutation, with dbias and for split tiles; one for n_tok tokens
- *           serves every call of that layer with fewer.
+ *   ws      used for split tiles, with dbias and with a permutation (n_tok *
+ *           d_col * 2 bytes rounded up to 256); *_workspace_size(n_tok, d_col,
+ *           d_row) bytes serve every call of that layer with up to n_tok tokens.
  *   n_tok == 0 writes nothing but a zero dbias.
  */
 gptq_status gptq_dequant_gemm_linear_backward(

@@ -419,9 +419,7 @@ gptq_status gptq_dequant_gemm_linear(const uint16_t* X, int64_t n_tok, int64_t d
     a.bias = bias; a.act = activation; a.residual = residual; a.ldr = ldr;
     a.pre[0] = pre; a.ldpre[0] = ldpre;
     a.Y = Y; a.ldy = ldy; a.status = dev_status; a.ws = ws;
-    if (gptq::linear_gemm_needs_workspace(a) &&
-        small_ws(ws, ws_bytes, gptq::linear_gemm_workspace_bytes(n_tok, d_col, d_row, false)))
-        return GPTQ_ERR_WORKSPACE;
+    if (small_ws(ws, ws_bytes, gptq::linear_gemm_call_bytes(a))) return GPTQ_ERR_WORKSPACE;
     return launch_status(gptq::launch_linear_gemm(a, stream));
 }
 
@@ -450,9 +448,7 @@ gptq_status gptq_dequant_gemm_gated(const uint16_t* X, int64_t n_tok, int64_t d_
     a.pre[0] = gate; a.ldpre[0] = ldgate;
     a.pre[1] = up; a.ldpre[1] = ldup;
     a.Y = Y; a.ldy = ldy; a.status = dev_status; a.ws = ws;
-    if (gptq::linear_gemm_needs_workspace(a) &&
-        small_ws(ws, ws_bytes, gptq::linear_gemm_workspace_bytes(n_tok, d_col, d_row, true)))
-        return GPTQ_ERR_WORKSPACE;
+    if (small_ws(ws, ws_bytes, gptq::linear_gemm_call_bytes(a))) return GPTQ_ERR_WORKSPACE;
     return launch_status(gptq::launch_linear_gemm(a, stream));
 }
 
@@ -484,9 +480,7 @@ gptq_status gptq_dequant_gemm_linear_backward(
     a.pre[0] = pre; a.ldpre[0] = ldpre;
     a.dP[0] = dPre; a.lddp[0] = lddpre;
     a.dbias = dbias; a.dX = dX; a.lddx = lddx; a.status = dev_status; a.ws = ws;
-    if (gptq::linear_backward_needs_workspace(a) &&
-        small_ws(ws, ws_bytes, gptq::linear_backward_workspace_bytes(n_tok, d_col, d_row, false)))
-        return GPTQ_ERR_WORKSPACE;
+    if (small_ws(ws, ws_bytes, gptq::linear_backward_call_bytes(a))) return GPTQ_ERR_WORKSPACE;
     return launch_status(gptq::launch_linear_backward(a, stream));
 }
 
@@ -516,9 +510,7 @@ gptq_status gptq_dequant_gemm_gated_backward(
     a.dP[0] = dGate; a.lddp[0] = lddgate;
     a.dP[1] = dUp; a.lddp[1] = lddup;
     a.dX = dX; a.lddx = lddx; a.status = dev_status; a.ws = ws;
-    if (gptq::linear_backward_needs_workspace(a) &&
-        small_ws(ws, ws_bytes, gptq::linear_backward_workspace_bytes(n_tok, d_col, d_row, true)))
-        return GPTQ_ERR_WORKSPACE;
+    if (small_ws(ws, ws_bytes, gptq::linear_backward_call_bytes(a))) return GPTQ_ERR_WORKSPACE;
     return launch_status(gptq::launch_linear_backward(a, stream));
 }
 

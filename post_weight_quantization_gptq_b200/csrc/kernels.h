@@ -155,7 +155,7 @@ gptq_status launch_linear_decode(const LinearCall& c, cudaStream_t stream);
 cudaError_t launch_gather_bf16(const uint16_t* X, int64_t ldx, int64_t n_tok, int d_col,
                                const int32_t* perm, uint16_t* Xq, cudaStream_t stream);
 size_t linear_gemm_workspace_bytes(int64_t n_tok, int64_t d_col, int64_t d_row, bool gated);
-bool linear_gemm_needs_workspace(const LinearCall& c);
+size_t linear_gemm_call_bytes(const LinearCall& c);   // what this call uses of it
 gptq_status launch_linear_gemm(const LinearCall& c, cudaStream_t stream);
 
 // ---- gradients (linear_backward.cu: slopes, bias sums and the column order;
@@ -184,7 +184,7 @@ gptq_status launch_slopes(const BackwardCall& c, float* bias_part, int64_t* laun
 gptq_status launch_scatter(const uint16_t* dXq, int64_t n_tok, int d_col, const int32_t* perm, uint16_t* dX,
                            int64_t lddx, cudaStream_t stream);
 size_t linear_backward_workspace_bytes(int64_t n_tok, int64_t d_col, int64_t d_row, bool gated);
-bool linear_backward_needs_workspace(const BackwardCall& c);
+size_t linear_backward_call_bytes(const BackwardCall& c);   // what this call uses of it
 gptq_status launch_linear_backward(const BackwardCall& c, cudaStream_t stream);
 
 // ---- stage 5 (pack.cu)

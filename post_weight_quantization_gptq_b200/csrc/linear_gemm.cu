@@ -1132,8 +1132,21 @@ size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 }  // namespace
 
 size_t linear_gemm_workspace_bytes(int64_t n_tok, int64_t d_col, int64_t d_row, bool gated) {
-    return round256(static_cast<size_t>(n_tok) * d_col * 2) +
-           round256(most_part_bytes(n_tok, d_row, static_cast<int>(d_col / BK), gated));
+    return round256(most_part_bytes(n_tok, d_row, static_cast<int>(d_col / BK), gated)) +
+           round256(static_cast<size_t>(n_tok) * d_col * 2);
+}
+
+namespace {
+// A call's workspace: its partial tiles, then the gathered tokens.
+size_t gemm_part_bytes(const LinearCall& c) {
+    return round256(make_plan(c.n_tok, c.d_row, static_cast<int>(c.d_col / BK), c.mat[1].packed != nullptr, c.bits == 3)
+                        .part_bytes);
+}
+}  // namespace
+
+size_t linear_gemm_call_bytes(const LinearCall& c) {
+    return gemm_part_bytes(c) +
+           (needs_gather(c.X, c.ldx, c.perm) ? round256(static_cast<size_t>(c.n_tok) * c.d_col * 2) : 0);
 }
 
 gptq_status launch_linear_gemm(const LinearCall& c, cudaStream_t stream) {
@@ -1142,7 +1155,7 @@ gptq_status launch_linear_gemm(const LinearCall& c, cudaStream_t stream) {
     const uint16_t* A = c.X;
     int64_t lda = c.ldx;
     if (needs_gather(c.X, c.ldx, c.perm)) {
-        uint16_t* xq = static_cast<uint16_t*>(c.ws);
+        uint16_t* xq = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(c.ws) + gemm_part_bytes(c));
         if (launch_gather_bf16(c.X, c.ldx, c.n_tok, static_cast<int>(c.d_col), c.perm, xq, stream) != cudaSuccess)
             return GPTQ_ERR_CUDA;
         A = xq;
@@ -1170,40 +1183,48 @@ gptq_status launch_linear_gemm(const LinearCall& c, cudaStream_t stream) {
     }
     a.Y = c.Y; a.ldy = c.ldy;
     a.status = c.status;
-    void* part = static_cast<uint8_t*>(c.ws) + round256(static_cast<size_t>(c.n_tok) * c.d_col * 2);
     const uint32_t* packed[2] = {c.mat[0].packed, gated ? c.mat[1].packed : c.mat[0].packed};
-    const gptq_status s = gated ? run<kGated>(a, ta, packed, c.bits, c.bits == 3, part, &launches, stream)
-                                : run<kLinear>(a, ta, packed, c.bits, c.bits == 3, part, &launches, stream);
+    const gptq_status s = gated ? run<kGated>(a, ta, packed, c.bits, c.bits == 3, c.ws, &launches, stream)
+                                : run<kLinear>(a, ta, packed, c.bits, c.bits == 3, c.ws, &launches, stream);
     count_launches(launches);
     return s;
 }
 
-// Whether the call reads its workspace at all.
-bool linear_gemm_needs_workspace(const LinearCall& c) {
-    const Plan p = make_plan(c.n_tok, c.d_row, static_cast<int>(c.d_col / BK), c.mat[1].packed != nullptr, c.bits == 3);
-    return p.part_bytes > 0 || needs_gather(c.X, c.ldx, c.perm);
-}
-
 // ---- gradients: the slopes (linear_backward.cu), then dXq = dP W here, then
-// the columns back in the input's order.  Workspace: dXq (with a permutation),
-// the partial tiles, the partial bias gradients.
+// the columns back in the input's order.
 namespace {
 int back_stages(int64_t d_row, bool gated) { return static_cast<int>((d_row + BK - 1) / BK) * (gated ? 2 : 1); }
+
+// A call's workspace: its partial tiles, the partial bias gradients, dXq (with a
+// permutation).
+struct BackwardSpace {
+    size_t at_bias, at_dxq, total;
+};
+BackwardSpace backward_space(const BackwardCall& c) {
+    const Plan p = make_plan(c.n_tok, c.d_col, back_stages(c.d_row, c.mat[1].packed != nullptr), false, false);
+    BackwardSpace w;
+    w.at_bias = round256(p.part_bytes);
+    w.at_dxq = w.at_bias + (c.dbias != nullptr ? round256(bias_partial_bytes(c.n_tok, c.d_row)) : 0);
+    w.total = w.at_dxq + (c.perm != nullptr ? round256(static_cast<size_t>(c.n_tok) * c.d_col * 2) : 0);
+    return w;
+}
 }  // namespace
 
 size_t linear_backward_workspace_bytes(int64_t n_tok, int64_t d_col, int64_t d_row, bool gated) {
-    return round256(static_cast<size_t>(n_tok) * d_col * 2) +
-           round256(most_part_bytes(n_tok, d_col, back_stages(d_row, gated), false)) +
-           (gated ? 0 : round256(most_bias_partial_bytes(n_tok, d_row)));
+    return round256(most_part_bytes(n_tok, d_col, back_stages(d_row, gated), false)) +
+           (gated ? 0 : round256(most_bias_partial_bytes(n_tok, d_row))) +
+           round256(static_cast<size_t>(n_tok) * d_col * 2);
 }
+
+size_t linear_backward_call_bytes(const BackwardCall& c) { return backward_space(c).total; }
 
 gptq_status launch_linear_backward(const BackwardCall& c, cudaStream_t stream) {
     const bool gated = c.mat[1].packed != nullptr;
     int64_t launches = 0;
     uint8_t* ws = static_cast<uint8_t*>(c.ws);
-    const size_t at_part = round256(static_cast<size_t>(c.n_tok) * c.d_col * 2);
-    const Plan p = make_plan(c.n_tok, c.d_col, back_stages(c.d_row, gated), false, false);
-    float* bias_part = c.dbias == nullptr ? nullptr : reinterpret_cast<float*>(ws + at_part + round256(p.part_bytes));
+    const BackwardSpace w = backward_space(c);
+    float* bias_part = c.dbias == nullptr ? nullptr : reinterpret_cast<float*>(ws + w.at_bias);
+    uint16_t* dxq = c.perm == nullptr ? nullptr : reinterpret_cast<uint16_t*>(ws + w.at_dxq);
     gptq_status s = launch_slopes(c, bias_part, &launches, stream);
     if (s != GPTQ_OK) return s;
     CUtensorMap ta[2];
@@ -1223,25 +1244,17 @@ gptq_status launch_linear_backward(const BackwardCall& c, cudaStream_t stream) {
     a.nk = back_stages(c.d_row, gated);
     a.nk1 = back_stages(c.d_row, false);
     a.g = (c.group == -1 || c.group > a.d_col) ? a.d_col : c.group;
-    a.Y = c.perm != nullptr ? reinterpret_cast<uint16_t*>(ws) : c.dX;
+    a.Y = c.perm != nullptr ? dxq : c.dX;
     a.ldy = c.perm != nullptr ? c.d_col : c.lddx;
     a.status = c.status;
     const uint32_t* packed[2] = {a.mat[0].packed, a.mat[1].packed};
-    s = run<kBack>(a, ta, packed, c.bits, false, ws + at_part, &launches, stream);
+    s = run<kBack>(a, ta, packed, c.bits, false, ws, &launches, stream);
     if (s == GPTQ_OK && c.perm != nullptr) {
-        s = launch_scatter(reinterpret_cast<const uint16_t*>(ws), c.n_tok, static_cast<int>(c.d_col), c.perm, c.dX,
-                           c.lddx, stream);
+        s = launch_scatter(dxq, c.n_tok, static_cast<int>(c.d_col), c.perm, c.dX, c.lddx, stream);
         ++launches;
     }
     count_launches(launches);
     return s;
-}
-
-// Whether the call reads its workspace at all.
-bool linear_backward_needs_workspace(const BackwardCall& c) {
-    const bool gated = c.mat[1].packed != nullptr;
-    const Plan p = make_plan(c.n_tok, c.d_col, back_stages(c.d_row, gated), false, false);
-    return c.perm != nullptr || p.part_bytes > 0 || c.dbias != nullptr;
 }
 
 }  // namespace gptq

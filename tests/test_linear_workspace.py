@@ -1,5 +1,5 @@
 """Workspaces of the tensor-core products with an epilogue: one that serves a
-batch serves every smaller one."""
+batch serves every smaller one, and a call needs no more than it uses."""
 import numpy as np
 import pytest
 import torch
@@ -78,3 +78,34 @@ def test_a_workspace_of_the_largest_batch_serves_the_smaller_ones(q, name):
         lt.check(Y, want[0], want[1], f"{n} tokens")
         assert q.gptq_sync_status(st) == 0
         assert bool((buf[size:] == 255).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,d_col,d_row", [(300, 4096, 300), (90, 2048, 260)])
+def test_a_call_that_only_splits_needs_no_room_for_its_tokens(q, n, d_col, d_row):
+    """Without a permutation the tokens are read where they are; with one the
+    same workspace is refused."""
+    rng, layers, _ = _setup(n, d_col, d_row, False)
+    perm = lt.cuda(rng.permutation(d_col).astype(np.int32))
+    dev = layers[0].cuda()
+    X, Y = lt.bf16(rng, n, d_col), _e(n, d_row)
+    ws = lt.workspace(q.gptq_dequant_gemm_linear_workspace_size(n, d_col, d_row) - n * d_col * 2)
+    q.gptq_dequant_gemm_linear(X.cuda(), *dev, None, 4, 128, Y, ws)
+    want = lt.linear(X, layers[0], None, "many")
+    lt.check(Y, want[0], want[1], "Y")
+    with pytest.raises(q.GPTQError) as e:
+        q.gptq_dequant_gemm_linear(X.cuda(), *dev, perm, 4, 128, Y, ws)
+    assert e.value.status == 6
+    # backward: the roles of the widths change places
+    layer = lt.Layer(d_col, 320, 4, 64, rng)
+    dY, dX = lt.bf16(rng, n, d_col), _e(n, 320)
+    size = q.gptq_dequant_gemm_linear_backward_workspace_size(n, 320, d_col)
+    slabs = -(-n // 8) * d_col * 4
+    ws = lt.workspace((size - n * 320 * 2 - slabs) // 256 * 256)
+    q.gptq_dequant_gemm_linear_backward(dY.cuda(), *layer.cuda(), None, 4, 64, dX, ws)
+    want = lt.back_product([dY], [layer], None)
+    lt.check(dX, want[0], want[1], "dX")
+    with pytest.raises(q.GPTQError) as e:
+        q.gptq_dequant_gemm_linear_backward(dY.cuda(), *layer.cuda(), None, 4, 64, dX, ws,
+                                            dbias=torch.empty(d_col, device="cuda"))
+    assert e.value.status == 6
