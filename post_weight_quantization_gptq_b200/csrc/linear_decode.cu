@@ -41,7 +41,7 @@
 
 #include "activation.cuh"
 #include "common.cuh"
-#include "dequant.cuh"
+#include "f32x2.cuh"
 #include "kernels.h"
 
 namespace cg = cooperative_groups;

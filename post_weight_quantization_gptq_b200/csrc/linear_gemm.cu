@@ -40,7 +40,7 @@
 
 #include "activation.cuh"
 #include "common.cuh"
-#include "dequant.cuh"
+#include "f32x2.cuh"
 #include "kernels.h"
 
 namespace gptq {
@@ -65,7 +65,10 @@ constexpr int kMaxPStages = 6;
 constexpr int kDeqWarps = kTeams * kTeamWarps;
 constexpr int kThreads = 32 * (3 + kDeqWarps);
 constexpr uint32_t kTmemCols = 256;
-constexpr int kSms = 148;                     // SMs of the device this library is built for
+// SMs of the device this library is built for.  It only shapes the plan (split
+// contractions, partial tiles): with fewer SMs a call is as right and takes more
+// waves, and a workspace's size does not depend on the current device.
+constexpr int kSms = 148;
 constexpr int kMinStages = 4;                 // least stages of a split tile's part (8: 4096 x 1024, 128 tokens 16.6 us, now 14.7)
 constexpr int kMaxSplit = 16;
 
@@ -104,10 +107,10 @@ struct Args {
     int nk;              // stages of the whole contraction
     int nk1;             // backward: stages of the first matrix
     int d_row, d_col, g;
-    int tiles_n, tiles_t;
+    int tiles_n;
     int full, split, per;   // whole tiles; parts of the others and their stages
     int part_rows;          // tokens of a partial tile
-    int tile_tokens;        // 256, or 512 per pair of CTAs
+    int tile_tokens;        // 128, or 512 per pair of CTAs
     float* part;
     const float* bias;
     int act;
@@ -335,9 +338,8 @@ __device__ __forceinline__ void weights8(const uint32_t (&w)[NW], int c, const G
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint64_t r = mul2(sub2(f[i], g.off[i % Group<BITS>::kPairs]), g.scale[i % Group<BITS>::kPairs]);
         float lo, hi;
-        asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(r));
+        unpk2(mul2(sub2(f[i], g.off[i % Group<BITS>::kPairs]), g.scale[i % Group<BITS>::kPairs]), lo, hi);
         o[i] = f32x2_to_bf16x2(lo, hi);
     }
 }
@@ -1094,7 +1096,7 @@ template <int MODE>
 gptq_status run(Args a, const CUtensorMap (&ta)[2], const uint32_t* const (&packed)[2], int bits, bool pairs,
                 void* part, int64_t* launches, cudaStream_t stream) {
     const Plan p = make_plan(a.n_tok, a.N, a.nk, MODE == kGated, pairs);
-    a.tiles_n = p.tiles_n; a.tiles_t = p.tiles_t;
+    a.tiles_n = p.tiles_n;
     a.full = p.full; a.split = p.split; a.per = p.per; a.part_rows = p.part_rows;
     a.tile_tokens = p.tile_tokens;
     a.part = static_cast<float*>(part);
