@@ -3,9 +3,12 @@
 // value overflows into a NaN for a finite x, and so that the small values left
 // of zero keep their relative accuracy (erfc and 1 / (1 + exp) instead of
 // 1 + erf and 1 + tanh).  exp and the quotient are CUDA's approximate forms: a
-// few units of 2^-23 plus the rounding of exp's argument, against 2^-8 of the
-// bf16 outputs (with the exact forms a 256 x 256 output tile spent 56 us in its
+// few units of 2^-23 plus the rounding of exp's argument.  Values go to bf16
+// outputs (2^-8; with the exact forms a 256 x 256 output tile spent 56 us in its
 // GELU, almost half of what its product takes; 16 us with one branch per value).
+// Slopes also enter the fp32 bias gradient: over every bf16 x they are within 2.8
+// units of 2^-24 of the true slope, where the formulas in plain fp32 with exact
+// exp and tanh are within 1.6 (GELU), 9 (GELU_TANH) and 16 (SILU).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -28,13 +31,26 @@ __device__ __forceinline__ float inv_one_plus_exp2(float y) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
     return r;
 }
+// ... and its product with one minus itself, p = 2^y / (1 + 2^y)^2, for the slopes
+// (as h (1 - h) it loses all bits where h comes near 1: a SILU slope was off by
+// 16 units of 2^-24, a GELU_TANH one by 32, and dbias is an fp32 output).  p is 0
+// where 2^y or 2^-y is out of range.
+__device__ __forceinline__ float logistic(float y, float& p) {
+    float e, h;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(y));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(h) : "f"(1.f + e));
+    p = h * (fminf(e, 0x1p125f) * h);   // (inf * 0 otherwise)
+    return h;
+}
 __device__ __forceinline__ float sigmoid_f(float x) { return inv_one_plus_exp2(-kLog2E * x); }
 
-// (1 + tanh(u)) / 2 = 1 / (1 + exp(-2u)), u = sqrt(2/pi) (x + 0.044715 x^3)
-__device__ __forceinline__ float gelu_tanh_half(float x) {
+// (1 + tanh(u)) / 2 = 1 / (1 + exp(-2u)), u = sqrt(2/pi) (x + 0.044715 x^3); the
+// exponent of 2 in it
+__device__ __forceinline__ float gelu_tanh_exponent(float x) {
     constexpr float k1 = -2.f * kLog2E * kSqrt2OverPi, k3 = k1 * kGeluCubic;
-    return inv_one_plus_exp2(x * fmaf(k3, x * x, k1));
+    return x * fmaf(k3, x * x, k1);
 }
+__device__ __forceinline__ float gelu_tanh_half(float x) { return inv_one_plus_exp2(gelu_tanh_exponent(x)); }
 
 __device__ __forceinline__ float activate(float x, int act) {
     switch (act) {
@@ -76,16 +92,16 @@ __device__ __forceinline__ float activate_slope(float x, int act) {
         case GPTQ_ACT_GELU:
             return 0.5f * erfcf(-x * kInvSqrt2) + x * kInvSqrt2Pi * __expf(-0.5f * x * x);
         case GPTQ_ACT_GELU_TANH: {
-            const float h = gelu_tanh_half(x), p = h * (1.f - h);
+            float p;
+            const float h = logistic(gelu_tanh_exponent(x), p);
             // p is 0 where x^2 may overflow
             return p == 0.f ? h
                             : h + 2.f * x * p * kSqrt2OverPi * (1.f + 3.f * kGeluCubic * x * x);
         }
         case GPTQ_ACT_SILU: {
-            const float s = sigmoid_f(x);
-            // x s (1 - s) with s = 0 or 1 beyond |x| = 88 / 17 (x may be infinite there)
-            const float p = s * (1.f - s);
-            return p == 0.f ? s : s + x * p;
+            float p;
+            const float s = logistic(-kLog2E * x, p);
+            return p == 0.f ? s : s + x * p;   // p is 0 where x may be infinite
         }
         default: return 1.f;
     }
