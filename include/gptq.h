@@ -399,8 +399,8 @@ typedef enum gptq_activation {
  *   16, 32, 64 or a multiple of 128); otherwise GPTQ_ERR_UNSUPPORTED.  X, Y and
  *   residual rows of any alignment and stride.  n_tok == 0 is a no-op, and
  *   nothing outside the n_tok x d_row entries of an output is written.
- *   An infinite or NaN activation makes its token's outputs NaN (or infinite);
- *   other tokens are unaffected.
+ *   An infinite or NaN activation makes its token's outputs NaN, infinite or
+ *   the activation's limit; other tokens are unaffected.
  *   Deterministic (no atomics); may be captured in a CUDA graph.  Calls that
  *   overlap on the GPU (two streams, two captured graphs) need a workspace each.
  *   Errors: GPTQ_ERR_INVALID_ARG for NULL pointers, bad sizes, strides or
@@ -442,7 +442,8 @@ size_t gptq_dequant_matmul_gated_workspace_size(int64_t n_tok, int64_t d_col);
 /*
  * Many-token form on the tensor cores.  The weights enter as the 16-bit numbers
  * W[n][k] = bf16_rne( fp32 scales[k/g][n] * (code[n][k] - zeros[k/g][n]) ), as in
- * gptq_dequant_gemm; sums are fp32.
+ * gptq_dequant_gemm (a scale of magnitude below 2^-114 may lose bits); sums are
+ * fp32.
  *   pre     linear, or NULL: n_tok x d_row bf16 output (leading dimension ldpre),
  *           the sums with the bias, before the activation, rounded to bf16:
  *           what the backward pass needs.

@@ -20,14 +20,17 @@
 // absolute, times s).
 //
 // Bound: the packed layer is read once for up to 32 tokens, so HBM; below
-// about 10 MB the launch and the length of one warp's chain.  What costs after
-// that is issue slots: at the measured copy rate an SM receives 46 4-bit codes
-// per cycle, 2.8 thread instructions each.  Which 16 codes meet in an
-// instruction is free as long as the tokens agree, so a lane takes 8
-// consecutive codes of two rows and masks them out with 5 shift / logic
-// instructions (7 where each pair is brought to the low bits and completed to
-// 128 + q); weights and tokens arrive by TMA, which costs the warps nothing
-// (per-thread asynchronous copies took 258 of 448 instructions per 4096 codes).
+// about 10 MB the launch and the length of one warp's chain.  A large layer
+// saturates no unit (8192 x 16384, one token: 40 % of HBM, 49 % of the issue
+// slots and of the ALU pipe while the SMs are busy, which is three quarters of
+// the time): what is left is few warps per SM, CTAs that do not fill the last
+// round, and the first loads and joins at its ends.  Instructions per code still
+// count.  Which 16 codes meet in an instruction is free as long as the tokens
+// agree, so a lane takes 8 consecutive codes of two rows and masks them out with
+// 5 shift / logic instructions (7 where each pair is brought to the low bits and
+// completed to 128 + q); weights and tokens arrive by TMA, which costs the warps
+// nothing (per-thread asynchronous copies took 258 of 448 instructions per 4096
+// codes).
 //
 // Work split: a warp owns 16 MT weight rows (gated: half of them of each
 // matrix) and every kth block of 128 codes, with a ring of blocks of its own in
@@ -56,7 +59,7 @@ constexpr int kMaxTok = 32;          // tokens per launch
 constexpr int kMaxDepth = 8;         // blocks of a warp's ring
 // Shared memory of two and of one CTA per SM: all of the 228 KB less 1 KB for
 // each CTA.  (With 112 KB the rings of groups of 64 at five to eight tokens missed two
-// blocks by 1 KB and ran with one CTA: 8192 x 8192 34.9 us, now 16.7.)
+// blocks by 1 KB and ran with one CTA: 8192 x 8192 34.9 us, now 17.1.)
 constexpr int kSmemTwo = 113 * 1024, kSmemOne = kMaxDynamicSmem;
 
 // How groups lie in a block of 128 codes: a block lies in one group; a group
@@ -687,13 +690,16 @@ cudaError_t launch_tokens(const Args& a, const Launch& l) {
     // a block's fixed work are shared by twice the weights: 8192 x 4096 at one
     // token 8.4 against 11.9 us with 32 rows), fewer where 32 rows are needed to
     // fill the GPU or where 64 leave no two blocks in the rings of two CTAs per SM
-    // (8192 x 8192, eight tokens: 8 bits in groups of 64 18.2 against 27.4, 4 bits in groups of 32
-    // 19.6 against 27.7 us).
+    // (8192 x 8192, eight tokens: 8 bits in groups of 64 18.5 against 27.4, 4 bits in groups of 32
+    // 19.8 against 27.7 us).
     constexpr int kMany = MODE == kTiny || BITS == 8 ? 2 : 4;
     if (a.n_tok <= 8 && (GATED ? 2 : 1) * static_cast<int64_t>(a.N) >= 4096 &&
         2 * ring_block_bytes<Shape<BITS, 1, kMany>>(a.n_tok, MODE == kWide ? 1 : kBlock / a.g) <= kSmemTwo - 1024)
         return launch_one<BITS, MODE, 1, kMany, GATED>(a, l);
     if (a.n_tok <= 8) return launch_one<BITS, MODE, 1, 2, GATED>(a, l);
+    // 9 to 16: 32 rows, two CTAs per SM; 64 rows run with one (8192 x 8192 at 16
+    // tokens 25.8 against 21.0 us, in groups of 32 33.2 against 27.1; ahead where
+    // the tiles go round several times, 2 x 28672 x 8192 104.9 against 115.2).
     if (a.n_tok <= 16) return launch_one<BITS, MODE, 2, 2, GATED>(a, l);
     // (wide codes or tiny groups: 64 rows would not leave room for two blocks)
     return launch_one<BITS, MODE, 4, MODE == kTiny || BITS == 8 ? 2 : 4, GATED>(a, l);
