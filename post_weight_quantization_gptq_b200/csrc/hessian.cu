@@ -260,10 +260,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------ epilogue warps 2..9
         const int q = warp & 3;  // TMEM lane quarter this warp may access
         const int half = (warp - 2) >> 2;  // which 128 of each accumulator's 256 columns it drains
+        bool ok = true;   // a lane whose wait runs out stays with its warp and adds nothing more
         for (int w = 0; w < waves; ++w) {
             const int t = blockIdx.x + (w / nchunk) * G;
             if (t >= num_blocks) break;
-            if (!warp_agree(!*abort && mbar_wait(&bars->acc_full, w & 1, abort))) break;
+            ok = ok && mbar_wait(&bars->acc_full, w & 1, abort);
             tc_fence_after();
             int pi, nj;
             block_coords(t, NT, pi, nj);
@@ -275,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int cc = half * (BN / 64); cc < (half + 1) * (BN / 64); ++cc) {
                     float v[32];
                     tmem_ld32(tmem + (static_cast<uint32_t>(q * 32) << 16) + h * BN + cc * 32, v);
-                    if (m < d) {
+                    if (ok && m < d) {
                         // all 32 loads in flight before any store (the
                         // compiler cannot prove the addresses distinct)
                         float hv[32];
